@@ -60,6 +60,35 @@ size_t atomattn_workspace_size(void);
 
 int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream);
 
+/* ---- Backward ----------------------------------------------------------------
+ * Gradients of a loss L through one atomattn_forward call with the same params.
+ * Given dout = dL/dout ([batch][n_atoms][heads][32], bf16), writes, in bf16, dq, dk
+ * and dv ([batch][n_atoms][heads][32]) and, where dbias is not NULL, dL/dbias (the
+ * layout of bias; 0 in slots that are not valid and in rows past the last atom).
+ * The probabilities are recomputed, so nothing is kept from the forward:
+ *
+ *   p = softmax over the valid slots, dp = dout . v, ds = p (dp - sum_s p dp)
+ *   dq = ds k / sqrt(32), dk = sum over queries of ds q / sqrt(32),
+ *   dv = sum over queries of p dout, dbias = ds
+ *
+ * A key atom's dk and dv add up over the windows that hold it; those of an atom
+ * with atom_mask 0 are 0, whatever its k and v hold (NaN included). A query
+ * without a valid slot, or whose logits are all -inf, gives no gradient. fp32
+ * logits, softmax and sums; p and ds enter the products as bf16. Sums are taken in
+ * a fixed order, so equal calls give equal bits.
+ *
+ * dout, dq, dk, dv and dbias must be 16-byte aligned and must not overlap an
+ * input, each other or the workspace. dbias without bias is an error. The atoms'
+ * gradients are written for every atom; nothing else is. All pointers must be
+ * memory of the current device. p->workspace holds the status word
+ * (atomattn_device_status); calls that may overlap in time need their own. */
+typedef struct atomattn_grads {
+    void *dq, *dk, *dv;
+    void *dbias;            /* or NULL */
+} atomattn_grads;
+
+int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn_grads *g, trimul_stream_t stream);
+
 /* Synchronises `stream`, then reads the status word: TRIMUL_OK, TRIMUL_ERR_TIMEOUT
  * or TRIMUL_ERR_DEVICE; detail[4] (optional) receives code, site, block, aux. */
 int atomattn_device_status(const atomattn_params *p, trimul_stream_t stream, int *detail);

@@ -35,7 +35,7 @@ STATUS = {
 }
 ERR = {v: k for k, v in STATUS.items()}
 
-# Every symbol include/trimul.h and include/atomattn.h declare.
+# Every symbol include/trimul.h, include/atomattn.h and include/linear.h declare.
 EXPORTS = ("trimul_workspace_size", "trimul_workspace_size_dtype", "trimul_forward", "trimul_prologue",
            "trimul_contract", "trimul_epilogue", "trimul_workspace_views", "trimul_device_status",
            "trimul_error_string", "trimul_last_error_detail", "trimul_version", "trimul_forward_noalloc",
@@ -44,7 +44,12 @@ EXPORTS = ("trimul_workspace_size", "trimul_workspace_size_dtype", "trimul_forwa
            "trimul_workspace_size_mxfp8", "trimul_forward_mxfp8", "trimul_contract_mxfp8", "trimul_mxfp8_views",
            "trimul_prologue_mxfp8", "trimul_mma_mxfp8",
            "trimul_shard_workspace_size", "trimul_prologue_rows", "trimul_contract_channels", "trimul_epilogue_rows",
-           "atomattn_forward", "atomattn_workspace_size", "atomattn_device_status")
+           "atomattn_forward", "atomattn_workspace_size", "atomattn_device_status", "atomattn_backward",
+           "trimul_linear_workspace_size", "trimul_linear_forward", "trimul_linear_backward_workspace_size",
+           "trimul_linear_backward", "trimul_linear_device_status", "trimul_act8_pack", "trimul_act8_unpack")
+
+# trimul_linear_params.act
+ACTS = {"none": 0, "relu": 1, "sigmoid": 2, "silu": 3}
 
 # Gradient outputs of trimul_grads, in struct order; each is "d_" + a TrimulParams field.
 GRAD_FIELDS = ("d_w_a", "d_w_ag", "d_w_b", "d_w_bg", "d_w_g", "d_w_o", "d_b_a", "d_b_ag", "d_b_b", "d_b_bg",
@@ -95,6 +100,28 @@ class AtomAttnParams(ctypes.Structure):
         ("bias", ctypes.c_void_p), ("atom_mask", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("timeout_ms", ctypes.c_uint32),
     ]
+
+
+class AtomAttnGrads(ctypes.Structure):
+    """Mirror of ``atomattn_grads`` in include/atomattn.h."""
+
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("dbias", ctypes.c_void_p)]
+
+
+class LinearParams(ctypes.Structure):
+    """Mirror of ``trimul_linear_params`` in include/linear.h."""
+
+    _fields_ = [
+        ("rows", ctypes.c_longlong), ("in_features", ctypes.c_int), ("out_features", ctypes.c_int),
+        ("act", ctypes.c_int), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("timeout_ms", ctypes.c_uint32),
+    ]
+
+
+class Act8Ptrs(ctypes.Structure):
+    """Mirror of ``trimul_act8`` in include/linear.h."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -149,6 +176,20 @@ def lib():
         L.atomattn_workspace_size.restype = S
         L.atomattn_forward.argtypes = [AP, P, P]
         L.atomattn_device_status.argtypes = [AP, P, ctypes.POINTER(ctypes.c_int)]
+        L.atomattn_backward.argtypes = [AP, P, ctypes.POINTER(AtomAttnGrads), P]
+        LP, LL = ctypes.POINTER(LinearParams), ctypes.c_longlong
+        L.trimul_linear_workspace_size.argtypes = []
+        L.trimul_linear_workspace_size.restype = S
+        L.trimul_linear_forward.argtypes = [P, P, LP, P, P]
+        L.trimul_linear_backward_workspace_size.argtypes = [LL, I, I, I, I]
+        L.trimul_linear_backward_workspace_size.restype = S
+        L.trimul_linear_backward.argtypes = [P, ctypes.POINTER(Act8Ptrs), P, LP, P, P, P, P]
+        L.trimul_linear_device_status.argtypes = [LP, P, ctypes.POINTER(ctypes.c_int)]
+        L.trimul_act8_pack.argtypes = [P, LL, I, P, P, P]
+        L.trimul_act8_unpack.argtypes = [P, P, LL, I, P, P]
+        for f in ("atomattn_backward", "trimul_linear_forward", "trimul_linear_backward", "trimul_linear_device_status",
+                  "trimul_act8_pack", "trimul_act8_unpack"):
+            getattr(L, f).restype = I
         for f in ("trimul_forward", "trimul_forward_noalloc", "trimul_prologue", "trimul_contract", "trimul_epilogue",
                   "trimul_workspace_views", "trimul_device_status", "trimul_version", "trimul_backward",
                   "atomattn_forward", "atomattn_device_status", "trimul_forward_mxfp8", "trimul_contract_mxfp8",
@@ -388,6 +429,276 @@ def atom_attention(q, k, v, bias=None, atom_mask=None, out=None, workspace=None,
     return out, p
 
 
+def atomattn_backward(params: AtomAttnParams, dout, grads: AtomAttnGrads, stream=None, check=True) -> int:
+    rc = lib().atomattn_backward(ctypes.byref(params), _ptr(dout), ctypes.byref(grads), _stream(stream))
+    if check:
+        _check(rc, "atomattn_backward")
+    return rc
+
+
+def _bf16(what: str, like, *tensors):
+    """Every tensor (None passes) must be contiguous bf16 on `like`'s CUDA device."""
+    import torch
+    for t in (like,) + tensors:
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous bf16")
+        if t.device != like.device or t.device.type != "cuda":
+            raise ValueError(f"{what}: tensors must be on one CUDA device")
+
+
+def _call_on(device, stream, inputs, call):
+    """``call(stream handle)`` with `device` current and, where a stream is given, that stream
+    current too, so that what the call allocates belongs to it. Inputs of other streams are
+    marked as used there: their memory is not handed out again before this work is done."""
+    import torch
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        out = call(s.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(s)
+        return out
+
+
+def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=None, stream=None):
+    """Gradients of sum(atom_attention(q, k, v, bias, atom_mask) * dout) (include/atomattn.h).
+
+    Arguments as for atom_attention, dout like q. Returns (dq, dk, dv, dbias), dbias None
+    without bias. A caller that gives `workspace` (atomattn_workspace_size() bytes) can read
+    the call's status there (device_status)."""
+    import torch
+    if q.dim() != 4 or q.shape[-1] != 32 or k.shape != q.shape or v.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("q, k, v, dout must be [batch, n_atoms, heads, 32] of one shape")
+    B, n, H, _ = q.shape
+    if bias is not None and tuple(bias.shape) != (B, (n + 31) // 32, H, 32, 128):
+        raise ValueError("bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
+    if atom_mask is not None and tuple(atom_mask.shape) != (B, n):
+        raise ValueError("atom_mask must be [batch, n_atoms]")
+    _bf16("atom_attention_backward", q, k, v, dout, bias, atom_mask)
+
+    def call(s):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+        dbias = None if bias is None else torch.empty_like(bias)
+        ws = workspace if workspace is not None else torch.empty(atomattn_workspace_size(), dtype=torch.uint8,
+                                                                 device=q.device)
+        p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask),
+                           ws.data_ptr(), ws.numel(), 0)
+        atomattn_backward(p, dout, AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias)), s)
+        return dq, dk, dv, dbias
+
+    return _call_on(q.device, stream, (q, k, v, dout, bias, atom_mask, workspace), call)
+
+
+# ---- linear layers and activations in 8 bits (include/linear.h) -----------------
+
+def trimul_linear_workspace_size() -> int:
+    return lib().trimul_linear_workspace_size()
+
+
+def trimul_linear_backward_workspace_size(rows: int, in_features: int, out_features: int, act: int,
+                                          from8: bool = False) -> int:
+    return lib().trimul_linear_backward_workspace_size(rows, in_features, out_features, act, int(from8))
+
+
+def trimul_linear_forward(x, residual, params: LinearParams, y, stream=None, check=True) -> int:
+    rc = lib().trimul_linear_forward(_ptr(x), _ptr(residual), ctypes.byref(params), _ptr(y), _stream(stream))
+    if check:
+        _check(rc, "trimul_linear_forward")
+    return rc
+
+
+def trimul_linear_backward(x, x8, dout, params: LinearParams, dx, dw, db, stream=None, check=True) -> int:
+    rc = lib().trimul_linear_backward(_ptr(x), None if x8 is None else ctypes.byref(x8), _ptr(dout),
+                                      ctypes.byref(params), _ptr(dx), _ptr(dw), _ptr(db), _stream(stream))
+    if check:
+        _check(rc, "trimul_linear_backward")
+    return rc
+
+
+def trimul_linear_device_status(params: LinearParams, stream=None):
+    """(code, [code, site, block, aux]) of the status word (synchronises)."""
+    d = (ctypes.c_int * 4)()
+    rc = lib().trimul_linear_device_status(ctypes.byref(params), _stream(stream), d)
+    return rc, list(d)
+
+
+def trimul_act8_pack(x, rows: int, channels: int, codes, scales, stream=None, check=True) -> int:
+    rc = lib().trimul_act8_pack(_ptr(x), rows, channels, _ptr(codes), _ptr(scales), _stream(stream))
+    if check:
+        _check(rc, "trimul_act8_pack")
+    return rc
+
+
+def trimul_act8_unpack(codes, scales, rows: int, channels: int, x, stream=None, check=True) -> int:
+    rc = lib().trimul_act8_unpack(_ptr(codes), _ptr(scales), rows, channels, _ptr(x), _stream(stream))
+    if check:
+        _check(rc, "trimul_act8_unpack")
+    return rc
+
+
+def device_status(workspace, stream=None):
+    """(code, [code, site, block, aux]) that the last call with this workspace left (synchronises):
+    linear, linear_backward or atom_attention_backward."""
+    p = LinearParams()
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return _call_on(workspace.device, stream, (), lambda s: trimul_linear_device_status(p, s))
+
+
+class Act8:
+    """A bf16 tensor kept in 8 bits: E4M3 codes (its shape, uint8) and one E8M0 scale per 32
+    channels (last dimension / 32, uint8). Made by act8_pack; act8_unpack gives the values, and
+    linear_backward and the triangle layers' backward take it in the tensor's place."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes, scales):
+        import torch
+        if codes.dim() < 1 or codes.shape[-1] % 32 or codes.shape[-1] == 0 or \
+                scales.shape != codes.shape[:-1] + (codes.shape[-1] // 32,):
+            raise ValueError("codes must be [..., channels] and scales [..., channels / 32]")
+        for t in (codes, scales):
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError("codes and scales must be contiguous uint8")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales = codes, scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def act8_pack(x, stream=None) -> Act8:
+    """Keep a bf16 tensor [..., channels] (channels a multiple of 32) in 33/32 bytes per value."""
+    import torch
+    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % 32:
+        raise ValueError("x must be [..., channels], channels a multiple of 32")
+    _bf16("act8_pack", x)
+    c = x.shape[-1]
+
+    def call(s):
+        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(x.shape[:-1] + (c // 32,), dtype=torch.uint8, device=x.device)
+        if x.numel():
+            trimul_act8_pack(x, x.numel() // c, c, codes, scales, s)
+        return Act8(codes, scales)
+
+    return _call_on(x.device, stream, (x,), call)
+
+
+def act8_unpack(a: Act8, out=None, stream=None):
+    """The values an Act8 stands for, as a bf16 tensor (written to `out` if given)."""
+    import torch
+    c = a.shape[-1]
+    if a.device.type != "cuda":
+        raise ValueError("act8_unpack: codes and scales must be on a CUDA device")
+    if out is not None:
+        if out.shape != a.shape or out.device != a.device:
+            raise ValueError("out must have the codes' shape and device")
+        _bf16("act8_unpack", out)
+
+    def call(s):
+        x = out if out is not None else torch.empty(a.shape, dtype=torch.bfloat16, device=a.device)
+        if x.numel():
+            trimul_act8_unpack(a.codes, a.scales, x.numel() // c, c, x, s)
+        return x
+
+    return _call_on(a.device, stream, (a.codes, a.scales, out), call)
+
+
+def _linear_shapes(what, x, weight, bias, act):
+    if weight.dim() != 2 or len(x.shape) < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"{what}: x must be [..., in_features] and weight [out_features, in_features]")
+    if bias is not None and tuple(bias.shape) != (weight.shape[0],):
+        raise ValueError(f"{what}: bias must be [out_features]")
+    if act not in ACTS:
+        raise ValueError(f"{what}: act must be one of {', '.join(ACTS)}")
+    return tuple(x.shape[:-1]) + (weight.shape[0],)
+
+
+def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=None, stream=None):
+    """act(x weight^T + bias) + residual in one kernel (include/linear.h), on bf16 device tensors.
+
+    x: [..., in_features]; weight: [out_features, in_features] (both multiples of 8); bias:
+    [out_features] or None; residual: like the result, or None; act: "none", "relu",
+    "sigmoid" or "silu". Returns out (allocated if None; it may be the residual itself). Not
+    recorded by autograd: linear_backward gives the gradients. A caller that gives
+    `workspace` (trimul_linear_workspace_size() bytes) can read the call's status there
+    (device_status)."""
+    import torch
+    shape = _linear_shapes("linear", x, weight, bias, act)
+    _bf16("linear", x, weight, bias, residual, out)
+    if residual is not None and tuple(residual.shape) != shape:
+        raise ValueError("linear: residual must have the result's shape")
+    if out is not None and tuple(out.shape) != shape:
+        raise ValueError("linear: out must have the result's shape")
+    n, k = weight.shape
+
+    def call(s):
+        y = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        if y.numel():
+            ws = workspace if workspace is not None else torch.empty(trimul_linear_workspace_size(), dtype=torch.uint8,
+                                                                     device=x.device)
+            p = LinearParams(y.numel() // n, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(),
+                             0)
+            trimul_linear_forward(x, residual, p, y, s)
+        return y
+
+    return _call_on(x.device, stream, (x, weight, bias, residual, out, workspace), call)
+
+
+def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_dw=True, need_db=True, workspace=None,
+                    stream=None):
+    """Gradients of sum(linear(x, weight, bias, act=act) * dout): (dx, dw, db), bf16 (include/linear.h).
+
+    x is the forward's input, or the Act8 that kept it. What is not needed is not computed
+    and comes back as None; db is computed without bias too (a bias of zeros). The
+    residual's gradient is dout itself. `workspace`: trimul_linear_backward_workspace_size
+    bytes, for callers that keep one or read the call's status from it (device_status)."""
+    import torch
+    held = isinstance(x, Act8)
+    shape = _linear_shapes("linear_backward", x, weight, bias, act)
+    if tuple(dout.shape) != shape:
+        raise ValueError("linear_backward: dout must be [..., out_features] with x's leading dimensions")
+    _bf16("linear_backward", weight, None if held else x, dout, bias)
+    if x.device != weight.device:
+        raise ValueError("linear_backward: tensors must be on one CUDA device")
+    n, k = weight.shape
+
+    def call(s):
+        new = lambda shape: torch.empty(shape, dtype=torch.bfloat16, device=weight.device)  # noqa: E731
+        dx = new(tuple(x.shape)) if need_dx else None
+        dw = new((n, k)) if need_dw else None
+        db = new((n,)) if need_db else None
+        rows = dout.numel() // n if n else 0
+        if rows == 0:  # nothing to sum over
+            for t in (dw, db):
+                if t is not None:
+                    t.zero_()
+            return dx, dw, db
+        need = trimul_linear_backward_workspace_size(rows, k, n, ACTS[act], held)
+        ws = workspace if workspace is not None else torch.empty(max(need, 256), dtype=torch.uint8,
+                                                                 device=weight.device)
+        p = LinearParams(rows, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
+        x8 = Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()) if held else None
+        trimul_linear_backward(None if held else x, x8, dout, p, dx, dw, db, s)
+        return dx, dw, db
+
+    tensors = (x.codes, x.scales) if held else (x,)
+    return _call_on(weight.device, stream, tensors + (weight, dout, bias, workspace), call)
+
+
 # ---- the layer as the pages use it ------------------------------------------
 
 # State-dict keys: (params field, key, required)
@@ -482,8 +793,14 @@ class _TriangleMultiplication:
         the workspace) and does not recompute them. block_rows gives the call
         only the workspace for blocks of that many rows
         (trimul_backward_workspace_size_rows); the library then uses the largest
-        block that fits in it."""
+        block that fits in it. z may be the Act8 that kept it since the forward
+        (33/32 bytes per value instead of 2): the gradients are then those at the
+        values it stands for."""
         import torch
+        if isinstance(z, Act8):
+            if reuse_forward:
+                raise ValueError("reuse_forward needs the z of the forward call, not the 8 bits kept of it")
+            z = act8_unpack(z, stream=stream)
         if z.dim() != 3 or z.shape[0] != z.shape[1] or z.shape[2] != self.c_z:
             raise ValueError("z must be [N, N, c_z]")
         if z.dtype != self.dtype or z.device != self.device or dout.shape != z.shape or dout.dtype != z.dtype:

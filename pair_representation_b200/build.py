@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libtrimul_b200.so")
 SOURCES = ["api.cu", "prologue_tc.cu", "contract_tc.cu", "epilogue_tc.cu", "simt_f32.cu", "noalloc.cu",
-           "backward.cu", "atomattn_tc.cu", "mx_tc.cu"]
+           "backward.cu", "atomattn_tc.cu", "mx_tc.cu", "atomattn_bwd.cu", "linear_tc.cu",
+           "act8.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tile_ops.cuh", "mx_block.cuh"]
 
 
@@ -34,7 +35,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [
-        os.path.join(ROOT, "include", h) for h in ("trimul.h", "atomattn.h")]
+        os.path.join(ROOT, "include", h) for h in ("trimul.h", "atomattn.h", "linear.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -13,6 +13,7 @@
 
 #include "atomattn.h"
 #include "kernels.h"
+#include "linear.h"
 #include "trimul.h"
 
 using namespace trimul;
@@ -85,7 +86,8 @@ int device_state(const DevState **out, bool need_tc) {
         if (d.cc_major == 10 && d.cc_minor == 0) {
             if ((e = prologue_tc_setup()) == cudaSuccess && (e = contract_tc_setup()) == cudaSuccess &&
                 (e = epilogue_tc_setup()) == cudaSuccess && (e = backward_setup()) == cudaSuccess &&
-                (e = atomattn_tc_setup()) == cudaSuccess)
+                (e = atomattn_tc_setup()) == cudaSuccess && (e = linear_tc_setup()) == cudaSuccess &&
+                (e = atomattn_bwd_setup()) == cudaSuccess)
                 e = contract_mx_setup();
             d.tc_setup = e;
         } else {
@@ -131,6 +133,31 @@ int check_device_ptr(const void *p, const char *name) {
     if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) {
         snprintf(g_detail, sizeof g_detail, "%s is not device memory", name);
         return TRIMUL_ERR_INVALID_ARG;
+    }
+    return TRIMUL_OK;
+}
+
+// Device memory, and of the current device: a kernel may not read another one's.
+int check_current_device(std::initializer_list<const void *> ptrs, const char *what) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) {
+        set_detail("cudaGetDevice", e);
+        return TRIMUL_ERR_CUDA;
+    }
+    for (const void *p : ptrs) {
+        if (!p) continue;
+        cudaPointerAttributes at;
+        if ((e = cudaPointerGetAttributes(&at, p)) != cudaSuccess) {
+            cudaGetLastError();
+            set_detail(what, e);
+            return TRIMUL_ERR_INVALID_ARG;
+        }
+        const bool here = at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+        if (!here) {
+            snprintf(g_detail, sizeof g_detail, "%s is not memory of device %d", what, dev);
+            return TRIMUL_ERR_INVALID_ARG;
+        }
     }
     return TRIMUL_OK;
 }
@@ -1099,6 +1126,29 @@ int check_attn(const atomattn_params *p, const void *out) {
     return TRIMUL_OK;
 }
 
+int check_attn_backward(const atomattn_params *p, const void *dout, const atomattn_grads *g) {
+    if (!g || !dout || !g->dk || !g->dv) return TRIMUL_ERR_INVALID_ARG;
+    if (int rc = check_attn(p, g->dq)) return rc;  // the params, and dq against the inputs
+    if (g->dbias && !p->bias) return TRIMUL_ERR_INVALID_ARG;
+    for (const void *v : {dout, static_cast<const void *>(g->dk), static_cast<const void *>(g->dv),
+                          static_cast<const void *>(g->dbias)})
+        if (v && !aligned(v, 16)) return TRIMUL_ERR_MISALIGNED;
+    const size_t n = attn_elems(p) * 2;
+    const size_t nb = (size_t)p->batch * attn_windows(p) * p->heads * 32 * 128 * 2;
+    const size_t nm = (size_t)p->batch * p->n_atoms * 2;
+    const std::pair<const void *, size_t> in[] = {{p->q, n}, {p->k, n}, {p->v, n}, {dout, n}, {p->bias, nb},
+                                                  {p->atom_mask, nm}};
+    const std::pair<const void *, size_t> out[] = {{g->dq, n}, {g->dk, n}, {g->dv, n}, {g->dbias, nb},
+                                                   {p->workspace, p->workspace_bytes}};
+    for (int i = 0; i < 5; ++i) {
+        for (auto &b : in)
+            if (overlap(out[i].first, out[i].second, b.first, b.second)) return TRIMUL_ERR_ALIAS;
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(out[i].first, out[i].second, out[j].first, out[j].second)) return TRIMUL_ERR_ALIAS;
+    }
+    return TRIMUL_OK;
+}
+
 // q, k or v [batch][n][heads][32] as (heads * 32, n, batch): boxes of one head's 32 elements x `rows`.
 int map_attn(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t rows) {
     const uint64_t row = (uint64_t)p->heads * 32;
@@ -1110,12 +1160,167 @@ int map_attn(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t r
 
 // bias [batch][n_windows][heads][32][128] as (slot, row, head, window, batch): boxes of one
 // window's 32 rows x 64 slots; windows past n_windows read as 0.
-int map_attn_bias(CUtensorMap *m, const atomattn_params *p) {
+int map_attn_bias(CUtensorMap *m, const void *t, const atomattn_params *p) {
     const uint64_t nw = (uint64_t)attn_windows(p), h = (uint64_t)p->heads;
     const uint64_t dims[5] = {128, 32, h, nw, (uint64_t)p->batch};
     const uint64_t strides[4] = {128 * 2, 32 * 128 * 2, h * 32 * 128 * 2, nw * h * 32 * 128 * 2};
     const uint32_t box[5] = {64, 32, 1, 1, 1};
-    return encode(m, 5, p->bias, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode(m, 5, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ---- linear layers ------------------------------------------------------------------
+
+constexpr int kMaxFeatures = 16384;
+constexpr long long kMaxRows = 1ll << 30;
+constexpr int kLinearCtas = 148;  // a B200's SMs: what the split products' workspace is sized for
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// Width of the column tiles. 256 halves the passes over A; but 128 where it covers the
+// columns with less padding, or where 256 would leave SMs without a tile.
+int linear_bn(long long M, int N) {
+    if (N <= 64) return 64;
+    const int c128 = ceil_div(N, 128), c256 = ceil_div(N, 256);
+    return c128 == 2 * c256 && (long long)ceil_div(M, 128) * c256 >= kLinearCtas ? 256 : 128;
+}
+
+// The parts of dW's contraction over the rows: as many as give every SM one output tile.
+struct LinearSplit {
+    int tiles, splits, per;  // 128 x 128 tiles of dW, parts, K blocks of 64 rows per part
+};
+LinearSplit linear_split(long long rows, int k, int n) {
+    LinearSplit s;
+    s.tiles = ceil_div(n, 128) * ceil_div(k, 128);
+    const int kb = ceil_div(rows, 64);
+    int want = kLinearCtas / s.tiles;
+    if (want < 1) want = 1;
+    if (want > kb) want = kb;
+    s.per = ceil_div(kb, want);
+    s.splits = ceil_div(kb, s.per);
+    return s;
+}
+
+// Sections of the backward workspace (byte offsets, 256-byte aligned).
+struct LinearBwdLayout {
+    size_t x, d, partial, sums, total;
+};
+LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int from8) {
+    LinearBwdLayout L;
+    size_t off = kHeader;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = round_up(off + bytes, 256);
+        return o;
+    };
+    L.x = take(from8 ? (size_t)rows * k * 2 : 0);                   // the values of x8, bf16
+    L.d = take(act != TRIMUL_ACT_NONE ? (size_t)rows * n * 2 : 0);  // D, bf16
+    const LinearSplit s = linear_split(rows, k, n);
+    L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
+    // Column sums of D: one row per part, or four per row-tile group of the D product.
+    const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * kLinearCtas : (size_t)s.splits;
+    L.sums = take(sums * n * 4);
+    L.total = off;
+    return L;
+}
+
+bool linear_sizes_ok(long long rows, int k, int n) {
+    return rows >= 1 && rows <= kMaxRows && k >= 1 && k <= kMaxFeatures && n >= 1 && n <= kMaxFeatures;
+}
+
+int check_linear(const trimul_linear_params *p, size_t need) {
+    if (!p->weight) return TRIMUL_ERR_INVALID_ARG;
+    if (!aligned(p->weight, 16) || (p->bias && !aligned(p->bias, 2))) return TRIMUL_ERR_MISALIGNED;
+    if (!p->workspace || p->workspace_bytes < need) return TRIMUL_ERR_WORKSPACE;
+    if (!aligned(p->workspace, 256)) return TRIMUL_ERR_MISALIGNED;
+    return TRIMUL_OK;
+}
+
+int check_linear_sizes(const trimul_linear_params *p) {
+    if (!p || !linear_sizes_ok(p->rows, p->in_features, p->out_features)) return TRIMUL_ERR_INVALID_ARG;
+    if (p->act < TRIMUL_ACT_NONE || p->act > TRIMUL_ACT_SILU) return TRIMUL_ERR_INVALID_ARG;
+    if (p->in_features % 8 || p->out_features % 8) return TRIMUL_ERR_UNSUPPORTED;
+    return TRIMUL_OK;
+}
+
+KernelCtl linear_ctl(const trimul_linear_params *p) {
+    KernelCtl c;
+    c.status = static_cast<DeviceStatus *>(p->workspace);
+    c.timeout_ns = (unsigned long long)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
+    c.debug_flags = 0;
+    return c;
+}
+
+// Matrix [rows][cols] of bf16 as an MMA operand (one batch).
+int map_operand(CUtensorMap *m, const void *t, int cols, int rows, bool mn, int tile_rows) {
+    return map_view(m, {t, (size_t)cols, 0}, cols, rows, 1, 64, mn ? 64 : (uint32_t)tile_rows, 2,
+                    CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
+    return map_view(m, {t, (size_t)cols, 0}, cols, rows, 1, 64, 32, 2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
+// Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. Returns the groups of row tiles
+// through *groups (LIN_GRAD's sums have four rows for each).
+int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, void *Y, int M, int N, int K, int act,
+               const void *bias, float *sums, bool clear, int *groups, const KernelCtl &ctl, const DevState &d,
+               cudaStream_t s) {
+    const int bn = linear_bn(M, N);
+    LinearMaps m;
+    if (int rc = map_operand(&m.a, A, K, M, false, 128)) return rc;
+    if (int rc = b_mn ? map_operand(&m.b, B, N, K, true, 0) : map_operand(&m.b, B, K, N, false, bn)) return rc;
+    if (int rc = map_blocks(&m.y, Y, N, M)) return rc;
+    m.e = m.y;  // unused without E
+    if (E)
+        if (int rc = map_blocks(&m.e, E, N, M)) return rc;
+    LinearArgs a;
+    memset(&a, 0, sizeof a);
+    a.M = M;
+    a.N = N;
+    a.b_mn = b_mn;
+    a.row_tiles = ceil_div(M, 128);
+    a.col_tiles = ceil_div(N, bn);
+    a.kblocks = ceil_div(K, 64);
+    a.groups = kLinearCtas / a.col_tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
+    if (a.groups > a.row_tiles) a.groups = a.row_tiles;
+    a.splits = 1;
+    a.kb_per_split = a.kblocks;
+    a.act = act;
+    a.has_e = E != nullptr;
+    a.bias = static_cast<const __nv_bfloat16 *>(bias);
+    a.sums = sums;
+    a.clear_status = clear ? 1 : 0;
+    a.ctl = ctl;
+    if (groups) *groups = a.groups;
+    return cuda_rc(launch_linear_tc(m, a, mode, bn, a.col_tiles * a.groups, s), "linear_tc launch");
+}
+
+// partial [splits][n][k] = D_s^T X_s over the rows of split s, in fp32; with sums, also the column
+// sums of D per split.
+int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long long rows, int k, int n, float *partial,
+                     float *sums, bool clear, const KernelCtl &ctl, const DevState &d, cudaStream_t s) {
+    LinearMaps m;
+    if (int rc = map_operand(&m.a, D, n, (int)rows, true, 0)) return rc;
+    if (int rc = map_operand(&m.b, X, k, (int)rows, true, 0)) return rc;
+    if (int rc = map_view(&m.y, {partial, (size_t)k, (size_t)n * k}, k, n, sp.splits, 32, 32, 4,
+                          CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+        return rc;
+    m.e = m.y;
+    LinearArgs a;
+    memset(&a, 0, sizeof a);
+    a.M = n;
+    a.N = k;
+    a.a_mn = a.b_mn = 1;
+    a.row_tiles = ceil_div(n, 128);
+    a.col_tiles = ceil_div(k, 128);
+    a.kblocks = ceil_div(rows, 64);
+    a.splits = sp.splits;
+    a.kb_per_split = sp.per;
+    a.sums = sums;
+    a.clear_status = clear ? 1 : 0;
+    a.ctl = ctl;
+    const long long units = (long long)sp.splits * sp.tiles;
+    const int grid = units < d.sms ? (int)units : d.sms;
+    return cuda_rc(launch_linear_tc(m, a, LIN_WG, 128, grid, s), "linear_tc launch");
 }
 
 }  // namespace
@@ -1398,7 +1603,7 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
         (rc = map_attn(&m.v, p->v, p, 256)))
         return rc;
     m.bias = m.q;  // unused without a bias
-    if (p->bias && (rc = map_attn_bias(&m.bias, p))) return rc;
+    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p))) return rc;
     AttnArgs a;
     a.batch = p->batch;
     a.n = p->n_atoms;
@@ -1415,6 +1620,41 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
     a.ctl.debug_flags = 0;
     const int grid = a.units < d->sms ? (int)a.units : d->sms;
     return cuda_rc(launch_atomattn_tc(m, a, grid, s), "atomattn_tc launch");
+}
+
+int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn_grads *g, trimul_stream_t stream) {
+    int rc;
+    if ((rc = check_attn_backward(p, dout, g))) return rc;
+    const DevState *d = nullptr;
+    if ((rc = device_state(&d, true))) return rc;
+    if ((rc = check_current_device({p->q, p->k, p->v, p->bias, p->atom_mask, p->workspace, dout, g->dq, g->dk, g->dv,
+                                    g->dbias},
+                                   "atom attention pointer")))
+        return rc;
+    AttnBwdMaps m;
+    if ((rc = map_attn(&m.q, p->q, p, 32)) || (rc = map_attn(&m.k, p->k, p, 32)) || (rc = map_attn(&m.v, p->v, p, 32)) ||
+        (rc = map_attn(&m.dout, dout, p, 32)))
+        return rc;
+    m.bias = m.dbias = m.q;  // unused without a bias
+    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p))) return rc;
+    if (g->dbias && (rc = map_attn_bias(&m.dbias, g->dbias, p))) return rc;
+    AttnBwdArgs a;
+    memset(&a, 0, sizeof a);
+    a.batch = p->batch;
+    a.n = p->n_atoms;
+    a.heads = p->heads;
+    a.n_windows = attn_windows(p);
+    a.has_bias = p->bias != nullptr;
+    a.has_dbias = g->dbias != nullptr;
+    a.mask = static_cast<const __nv_bfloat16 *>(p->atom_mask);
+    a.dq = static_cast<__nv_bfloat16 *>(g->dq);
+    a.dk = static_cast<__nv_bfloat16 *>(g->dk);
+    a.dv = static_cast<__nv_bfloat16 *>(g->dv);
+    a.scale = 0.17677669529663687f;  // 1 / sqrt(32)
+    a.ctl.status = static_cast<DeviceStatus *>(p->workspace);
+    a.ctl.timeout_ns = (unsigned long long)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
+    a.ctl.debug_flags = 0;
+    return cuda_rc(launch_atomattn_bwd(m, a, d->sms, reinterpret_cast<cudaStream_t>(stream)), "atomattn_bwd launch");
 }
 
 int atomattn_device_status(const atomattn_params *p, trimul_stream_t stream, int *detail) {
@@ -1434,6 +1674,150 @@ int atomattn_device_status(const atomattn_params *p, trimul_stream_t stream, int
     }
     if (st.code == DEV_OK) return TRIMUL_OK;
     return st.code == DEV_TIMEOUT ? TRIMUL_ERR_TIMEOUT : TRIMUL_ERR_DEVICE;
+}
+
+// ---- linear layers and activations in 8 bits (include/linear.h) ----------------------
+
+size_t trimul_linear_workspace_size(void) { return kHeader; }
+
+int trimul_linear_forward(const void *x, const void *residual, const trimul_linear_params *p, void *y,
+                          trimul_stream_t stream) {
+    int rc;
+    if ((rc = check_linear_sizes(p))) return rc;
+    if (!x || !y) return TRIMUL_ERR_INVALID_ARG;
+    if ((rc = check_linear(p, kHeader))) return rc;
+    for (const void *v : {x, residual, static_cast<const void *>(y)})
+        if (v && !aligned(v, 16)) return TRIMUL_ERR_MISALIGNED;
+    const size_t xn = (size_t)p->rows * p->in_features * 2, yn = (size_t)p->rows * p->out_features * 2;
+    const size_t wn = (size_t)p->in_features * p->out_features * 2, bn = (size_t)p->out_features * 2;
+    // The residual may be y itself (each block is read before it is written), not part of it.
+    if (overlap(y, yn, x, xn) || (residual != y && overlap(y, yn, residual, yn)) || overlap(y, yn, p->weight, wn) ||
+        overlap(y, yn, p->bias, bn) || overlap(y, yn, p->workspace, p->workspace_bytes) ||
+        overlap(p->workspace, kHeader, x, xn) || overlap(p->workspace, kHeader, residual, yn) ||
+        overlap(p->workspace, kHeader, p->weight, wn) || overlap(p->workspace, kHeader, p->bias, bn))
+        return TRIMUL_ERR_ALIAS;
+    const DevState *d = nullptr;
+    if ((rc = device_state(&d, true))) return rc;
+    if ((rc = check_current_device({x, residual, y, p->weight, p->bias, p->workspace}, "linear pointer"))) return rc;
+    return run_linear(LIN_FWD, x, p->weight, 0, residual, y, (int)p->rows, p->out_features, p->in_features, p->act,
+                      p->bias, nullptr, true, nullptr, linear_ctl(p), *d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t trimul_linear_backward_workspace_size(long long rows, int in_features, int out_features, int act, int from8) {
+    if (!linear_sizes_ok(rows, in_features, out_features) || in_features % (from8 ? 32 : 8) || out_features % 8 ||
+        act < TRIMUL_ACT_NONE || act > TRIMUL_ACT_SILU)
+        return 0;
+    return linear_bwd_layout(rows, in_features, out_features, act, from8).total;
+}
+
+int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy, const trimul_linear_params *p,
+                           void *dx, void *dw, void *db, trimul_stream_t stream) {
+    int rc;
+    if ((rc = check_linear_sizes(p))) return rc;
+    if (!dy || (x != nullptr) == (x8 != nullptr) || (x8 && (!x8->codes || !x8->scales))) return TRIMUL_ERR_INVALID_ARG;
+    if (x8 && p->in_features % 32) return TRIMUL_ERR_UNSUPPORTED;
+    const long long rows = p->rows;
+    const int k = p->in_features, n = p->out_features, act = p->act;
+    const LinearBwdLayout L = linear_bwd_layout(rows, k, n, act, x8 != nullptr);
+    if ((rc = check_linear(p, L.total))) return rc;
+    const void *codes = x8 ? x8->codes : nullptr, *scales = x8 ? x8->scales : nullptr;
+    for (const void *v : {x, codes, scales, dy, static_cast<const void *>(dx), static_cast<const void *>(dw)})
+        if (v && !aligned(v, 16)) return TRIMUL_ERR_MISALIGNED;
+    if (db && !aligned(db, 2)) return TRIMUL_ERR_MISALIGNED;
+    const size_t xn = (size_t)rows * k * 2, yn = (size_t)rows * n * 2, wn = (size_t)n * k * 2, bn = (size_t)n * 2;
+    const std::pair<const void *, size_t> in[] = {{x, xn}, {codes, (size_t)rows * k}, {scales, (size_t)rows * (k / 32)},
+                                                  {dy, yn}, {p->weight, wn}, {p->bias, bn}};
+    const std::pair<const void *, size_t> out[] = {{dx, xn}, {dw, wn}, {db, bn}, {p->workspace, p->workspace_bytes}};
+    for (int i = 0; i < 4; ++i) {
+        for (auto &b : in)
+            if (overlap(out[i].first, out[i].second, b.first, b.second)) return TRIMUL_ERR_ALIAS;
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(out[i].first, out[i].second, out[j].first, out[j].second)) return TRIMUL_ERR_ALIAS;
+    }
+    const DevState *d = nullptr;
+    if ((rc = device_state(&d, true))) return rc;
+    if ((rc = check_current_device({x, codes, scales, dy, dx, dw, db, p->weight, p->bias, p->workspace},
+                                   "linear pointer")))
+        return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *base = static_cast<uint8_t *>(p->workspace);
+    const KernelCtl ctl = linear_ctl(p);
+    if ((rc = cuda_rc(cudaMemsetAsync(base, 0, sizeof(DeviceStatus), s), "status clear"))) return rc;
+    const bool d_pass = act != TRIMUL_ACT_NONE && (dx || dw || db);
+    if (x8 && (dw || db || d_pass)) {
+        if ((rc = cuda_rc(launch_act8_unpack(codes, scales, base + L.x, rows * k, d->sms, s), "act8_unpack launch")))
+            return rc;
+        x = base + L.x;
+    }
+    float *sums = reinterpret_cast<float *>(base + L.sums), *partial = reinterpret_cast<float *>(base + L.partial);
+    const LinearSplit sp = linear_split(rows, k, n);
+    const void *D = dy;
+    int sum_rows = sp.splits;
+    if (d_pass) {
+        int groups = 0;
+        if ((rc = run_linear(LIN_GRAD, x, p->weight, 0, dy, base + L.d, (int)rows, n, k, act, p->bias,
+                             db ? sums : nullptr, false, &groups, ctl, *d, s)))
+            return rc;
+        D = base + L.d;
+        sum_rows = 4 * groups;
+    }
+    if (dx && (rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr,
+                               false, nullptr, ctl, *d, s)))
+        return rc;
+    const bool rows_sum = db && !d_pass;  // D is dy: its sums come with the weight product
+    if (dw || rows_sum) {
+        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, rows_sum ? sums : nullptr, false, ctl, *d, s)))
+            return rc;
+    }
+    LinearReduceArgs r;
+    memset(&r, 0, sizeof r);
+    r.partial = partial;
+    r.dw = static_cast<__nv_bfloat16 *>(dw);
+    r.count = (long long)n * k;
+    r.splits = sp.splits;
+    r.sums = sums;
+    r.db = static_cast<__nv_bfloat16 *>(db);
+    r.n = n;
+    r.sum_rows = sum_rows;
+    return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");
+}
+
+int trimul_linear_device_status(const trimul_linear_params *p, trimul_stream_t stream, int *detail) {
+    if (!p) return TRIMUL_ERR_INVALID_ARG;
+    atomattn_params q;
+    memset(&q, 0, sizeof q);
+    q.workspace = p->workspace;
+    return atomattn_device_status(&q, stream, detail);
+}
+
+static int check_act8(const void *x, long long rows, int channels, const void *codes, const void *scales) {
+    if (!x || !codes || !scales || rows < 1 || rows > kMaxRows || channels < 1 || channels > kMaxFeatures)
+        return TRIMUL_ERR_INVALID_ARG;
+    if (channels % 32) return TRIMUL_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return TRIMUL_ERR_MISALIGNED;
+    const size_t n = (size_t)rows * channels;
+    if (overlap(x, 2 * n, codes, n) || overlap(x, 2 * n, scales, n / 32) || overlap(codes, n, scales, n / 32))
+        return TRIMUL_ERR_ALIAS;
+    return TRIMUL_OK;
+}
+
+int trimul_act8_pack(const void *x, long long rows, int channels, void *codes, void *scales, trimul_stream_t stream) {
+    int rc;
+    if ((rc = check_act8(x, rows, channels, codes, scales))) return rc;
+    const DevState *d = nullptr;
+    if ((rc = device_state(&d, true)) || (rc = check_current_device({x, codes, scales}, "act8 pointer"))) return rc;
+    return cuda_rc(launch_act8_pack(x, codes, scales, rows * channels, d->sms, reinterpret_cast<cudaStream_t>(stream)),
+                   "act8_pack launch");
+}
+
+int trimul_act8_unpack(const void *codes, const void *scales, long long rows, int channels, void *x,
+                       trimul_stream_t stream) {
+    int rc;
+    if ((rc = check_act8(x, rows, channels, codes, scales))) return rc;
+    const DevState *d = nullptr;
+    if ((rc = device_state(&d, true)) || (rc = check_current_device({x, codes, scales}, "act8 pointer"))) return rc;
+    return cuda_rc(launch_act8_unpack(codes, scales, x, rows * channels, d->sms, reinterpret_cast<cudaStream_t>(stream)),
+                   "act8_unpack launch");
 }
 
 const char *trimul_error_string(int code) {

@@ -17,7 +17,8 @@ enum DeviceCode : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_FAULT = 2 };
 
 // Where a wait gave up: kernel id * 16 + site.
 enum Site : int {
-    SITE_PRO = 0x10, SITE_CON = 0x20, SITE_EPI = 0x30, SITE_ATT = 0x40,
+    SITE_PRO = 0x10, SITE_CON = 0x20, SITE_EPI = 0x30, SITE_ATT = 0x40, SITE_LIN = 0x50,
+    SITE_ATB = 0x60,
 };
 
 struct DeviceStatus {
@@ -187,6 +188,14 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
                  "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
+}
+
+__device__ __forceinline__ void tma_store_5d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, int c3,
+                                             int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5, %6}], [%1];" ::"l"(map),
+        "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }

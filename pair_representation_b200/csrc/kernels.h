@@ -266,6 +266,75 @@ size_t atomattn_tc_smem();
 cudaError_t atomattn_tc_setup();
 cudaError_t launch_atomattn_tc(const AttnMaps &m, const AttnArgs &a, int grid, cudaStream_t s);
 
+// ---- its gradients (atomattn_bwd.cu) -------------------------------------------
+
+struct AttnBwdArgs {
+    int batch, n, heads, n_windows;
+    int has_bias, has_dbias;
+    const __nv_bfloat16 *mask;        // [batch][n] or null
+    __nv_bfloat16 *dq, *dk, *dv;      // [batch][n][heads][32]
+    float scale;                      // 1 / sqrt(32)
+    int per_chain, chains;            // set by the launcher: key groups per block, blocks per (batch, head)
+    KernelCtl ctl;
+};
+
+struct AttnBwdMaps {
+    CUtensorMap q, k, v, dout;  // 3-D (heads * 32, n, batch), boxes (32, 32, 1), swizzle 64B
+    CUtensorMap bias, dbias;    // as AttnMaps::bias
+};
+
+cudaError_t atomattn_bwd_setup();
+cudaError_t launch_atomattn_bwd(const AttnBwdMaps &m, AttnBwdArgs a, int sms, cudaStream_t s);
+
+// ---- linear layers (linear_tc.cu) ----------------------------------------------
+
+enum LinearMode { LIN_FWD = 0, LIN_GRAD = 1, LIN_WG = 2 };
+enum LinearAct { LIN_NONE = 0, LIN_RELU = 1, LIN_SIGMOID = 2, LIN_SILU = 3 };  // enum trimul_act
+
+// Y[m][n] from A(m, k) and B(n, k) in 128 x BN tiles (see linear_tc.cu for the modes).
+struct LinearArgs {
+    int M, N;                  // rows and columns of Y
+    int a_mn, b_mn;            // operand stored [k][rows] instead of [rows][k]
+    int row_tiles, col_tiles, kblocks;
+    int groups;                // LIN_FWD, LIN_GRAD: CTA c owns column tile c % col_tiles and the row tiles
+                               // c / col_tiles, + groups, ...
+    int splits, kb_per_split;  // LIN_WG: the contraction in `splits` parts
+    int act, has_e;
+    const __nv_bfloat16 *bias;  // [N] or null
+    float *sums;  // LIN_GRAD: [groups * 4][N] column sums of Y; LIN_WG: [splits][M] row sums of A; or null
+    int clear_status;
+    KernelCtl ctl;
+};
+
+struct LinearMaps {
+    CUtensorMap a, b;  // 64 k x 128 rows (b: BN rows), or 64 rows x 64 k when MN-major; swizzle 128B
+    CUtensorMap e, y;  // blocks of 32 rows x 128 bytes, swizzle 128B
+};
+
+// dw[i] = bf16(sum_s partial[s][i]), db[j] = bf16(sum_s sums[s][j]); either may be null.
+struct LinearReduceArgs {
+    const float *partial;
+    __nv_bfloat16 *dw;
+    long long count;  // elements of dw
+    int splits;
+    const float *sums;
+    __nv_bfloat16 *db;
+    int n, sum_rows;
+    int weight_blocks;  // set by the launcher
+};
+
+cudaError_t linear_tc_setup();
+// Whether a BN-wide slab of B with this many K blocks stays in shared memory.
+bool linear_resident(int bn, int kblocks);
+cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, cudaStream_t s);
+cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s);
+
+// ---- activations in 8 bits (act8.cu); values: a multiple of 32 -------------------
+
+cudaError_t launch_act8_pack(const void *x, void *codes, void *scales, long long values, int sms, cudaStream_t s);
+cudaError_t launch_act8_unpack(const void *codes, const void *scales, void *x, long long values, int sms,
+                               cudaStream_t s);
+
 // ---- static scratch of trimul_forward_noalloc (noalloc.cu) --------------------
 
 // Device address of the library's static scratch array on the current device;

@@ -1,0 +1,576 @@
+// linear_tc.cu - a linear layer with its epilogue, and the three products of its
+// backward, on tcgen05 tensor cores.
+//
+//   LIN_FWD   Y = act(A B^T + bias) + E           (E: the residual, optional)
+//   LIN_GRAD  Y = E * act'(A B^T + bias)          (E: dL/dy; column sums of Y before
+//                                                  rounding give dL/dbias)
+//   LIN_WG    Y_s = A_s B_s^T in fp32             (split s of the contraction; with an
+//                                                  optional column of ones: row sums of A)
+//
+// A(m, k) and B(n, k) are bf16, each K-major ([rows][k]) or MN-major ([k][rows]): the
+// forward reads x and W K-major, dx = D W reads W MN-major, dW = D^T x reads both
+// MN-major with the rows of the batch as the contracted index.
+//
+// What bounds it: at the widths of a pair or atom representation (128 to 512 channels)
+// a row moves 2 (k + n) bytes for 2 k n operations, under the card's ratio of about 260
+// operations per byte, so the batch's rows are streamed once and everything else stays
+// on chip. A CTA owns one column tile (BN wide) and walks down the row tiles: with
+// kResident its slab of B (at most 64 KB) is loaded once and stays in shared memory;
+// only A tiles travel, through a ring. Wider contractions stream A and B together.
+// The accumulator is double-buffered in tensor memory (2 x BN columns) and drained by
+// eight warps, each storing its own 32 x 64 blocks by TMA, so the drain of one tile
+// overlaps the loads and MMAs of the next. E blocks arrive by TMA in the very buffer
+// the result leaves from, one block ahead.
+//
+// Every wait is bounded; on a timeout the CTA lets its copies land and returns.
+#include "kernels.h"
+
+namespace trimul {
+namespace lin {
+constexpr int BM = 128, BK = 64;
+constexpr int A_BYTES = BM * BK * 2;        // 16 KB
+constexpr int EPI_WARPS = 8;                // two per tensor-memory lane quarter
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr int WBUF = 4096;                  // 32 rows x 128 bytes
+constexpr int OUT_BYTES = EPI_WARPS * 2 * WBUF;
+constexpr int BIAS_BYTES = EPI_WARPS * 128 * 4;  // each drain warp's own copy of its columns' bias
+constexpr int ONES_BYTES = 16 * BK * 2;     // 16 rows of ones (LIN_WG)
+constexpr int BAR_BYTES = 512;
+constexpr int RES_BYTES = 65536;            // resident slab of B
+constexpr int TMEM_COLS = 512;
+constexpr int ONES_COL = 256;               // LIN_WG (BN = 128): accumulators of the ones column
+
+__host__ __device__ constexpr int stages(int bn, bool res) { return res ? 5 : bn == 256 ? 3 : 4; }
+__host__ __device__ constexpr int stage_bytes(int bn, bool res) { return A_BYTES + (res ? 0 : bn * BK * 2); }
+__host__ __device__ constexpr size_t smem(int bn, bool res) {
+    return 1024 + (size_t)stages(bn, res) * stage_bytes(bn, res) + (res ? RES_BYTES : 0) + OUT_BYTES + BIAS_BYTES +
+           ONES_BYTES + BAR_BYTES;
+}
+static_assert(smem(256, false) <= 232448 && smem(256, true) <= 232448 && smem(128, false) <= 232448, "shared memory");
+
+// The tiles of one CTA, in the order every role of the CTA visits them.
+template <int MODE>
+struct Tiles {
+    const LinearArgs &a;
+    int ct, rt, kb0, kb1, split;  // column tile, row tile, K blocks, split of the contraction
+    long long u;
+    __device__ explicit Tiles(const LinearArgs &args) : a(args), ct(0), rt(-1), kb0(0), kb1(args.kblocks), split(0), u(-1) {}
+    __device__ bool next() {
+        if (MODE == LIN_WG) {
+            u = u < 0 ? (long long)blockIdx.x : u + gridDim.x;
+            const int per = a.row_tiles * a.col_tiles;
+            if (u >= (long long)per * a.splits) return false;
+            split = (int)(u / per);
+            const int r = (int)(u - (long long)split * per);
+            rt = r / a.col_tiles;
+            ct = r - rt * a.col_tiles;
+            kb0 = split * a.kb_per_split;
+            kb1 = min(a.kblocks, kb0 + a.kb_per_split);
+            return true;
+        }
+        if (rt < 0) {
+            ct = (int)blockIdx.x % a.col_tiles;
+            rt = (int)blockIdx.x / a.col_tiles;
+        } else {
+            rt += a.groups;
+        }
+        return rt < a.row_tiles;
+    }
+};
+}  // namespace lin
+
+namespace {
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// exp(-p) and 1 / (1 + exp(-p)) by the hardware's ex2 and rcp (relative errors about 2^-22), far
+// under the half step 2^-9 of the bf16 result. NaN stays NaN.
+__device__ __forceinline__ float exp_neg(float p) { return ex2f(p * -1.4426950408889634f); }
+
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float p) {
+    if (ACT == LIN_RELU) return max_nan(p, 0.f);
+    if (ACT == LIN_NONE) return p;
+    const float s = rcpf(1.f + exp_neg(p));  // 0 where exp(-p) is infinite
+    return ACT == LIN_SIGMOID ? s : p * s;
+}
+
+// 1 - s is taken as s exp(-p), which keeps its digits where s is next to 1. p stops at -87, where
+// both factors are still finite and every slope is under 2e-36.
+template <int ACT>
+__device__ __forceinline__ float act_grad(float p, float d) {
+    if (ACT == LIN_RELU) return p > 0.f ? d : 0.f;
+    if (ACT == LIN_NONE) return d;
+    p = max_nan(p, -87.f);
+    const float e = exp_neg(p), s = rcpf(1.f + e), c = s * e;
+    return ACT == LIN_SIGMOID ? d * (s * c) : d * fmaf(p * s, c, s);
+}
+
+// The 64 columns of one accumulator row: + bias, activation, residual (or the gradient), packed
+// to bf16 into the row's 128 swizzled bytes. In LIN_GRAD v receives the unrounded values.
+template <int MODE, int ACT>
+__device__ __forceinline__ void finish_row(uint32_t (&v)[64], const float *bias, bool has_e, uint8_t *row, int x7) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ x7) << 4));
+        uint4 ev = make_uint4(0u, 0u, 0u, 0u);
+        if (has_e) ev = *at;
+        const uint32_t ew[4] = {ev.x, ev.y, ev.z, ev.w};
+        const float4 b0 = *reinterpret_cast<const float4 *>(bias + 8 * c);
+        const float4 b1 = *reinterpret_cast<const float4 *>(bias + 8 * c + 4);
+        const float bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int j = 8 * c + 2 * t;
+            const float e0 = __uint_as_float(ew[t] << 16), e1 = __uint_as_float(ew[t] & 0xFFFF0000u);
+            float y0 = __uint_as_float(v[j]) + bw[2 * t], y1 = __uint_as_float(v[j + 1]) + bw[2 * t + 1];
+            if (MODE == LIN_GRAD) {
+                y0 = act_grad<ACT>(y0, e0);
+                y1 = act_grad<ACT>(y1, e1);
+                v[j] = __float_as_uint(y0);
+                v[j + 1] = __float_as_uint(y1);
+            } else {
+                y0 = act_fwd<ACT>(y0) + e0;
+                y1 = act_fwd<ACT>(y1) + e1;
+            }
+            o[t] = pack_bf16x2(y0, y1);
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <int MODE>
+__device__ __forceinline__ void finish(int act, uint32_t (&v)[64], const float *bias, bool has_e, uint8_t *row, int x7) {
+    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(v, bias, has_e, row, x7);
+    else if (act == LIN_RELU) finish_row<MODE, LIN_RELU>(v, bias, has_e, row, x7);
+    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(v, bias, has_e, row, x7);
+    else finish_row<MODE, LIN_SILU>(v, bias, has_e, row, x7);
+}
+
+// Sums of 32 columns over the warp's 32 lanes: lane l returns column l's sum. Each step halves
+// the columns a lane holds (lanes with the bit set keep the upper half): 31 shuffles in all,
+// and the order of the additions is fixed.
+__device__ __forceinline__ float column_sum32(const uint32_t *v, int lane) {
+    float s[16];
+    const bool hi = (lane & 16) != 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float keep = __uint_as_float(hi ? v[i + 16] : v[i]), give = __uint_as_float(hi ? v[i] : v[i + 16]);
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    }
+#pragma unroll
+    for (int w = 8; w >= 1; w >>= 1) {
+        const bool up = (lane & w) != 0;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float keep = up ? s[i + w] : s[i], give = up ? s[i] : s[i + w];
+            s[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+    }
+    return s[0];
+}
+
+}  // namespace
+
+template <int BN, bool kResident, int MODE>
+__global__ void __launch_bounds__(lin::THREADS, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmY,
+                     const LinearArgs args) {
+    using namespace lin;
+    constexpr int STAGES = stages(BN, kResident), STAGE_BYTES = stage_bytes(BN, kResident);
+    constexpr int B_BYTES = BN * BK * 2;
+    constexpr int CHUNK = MODE == LIN_WG ? 32 : 64;  // accumulator columns per stored 128-byte row
+    constexpr int CHUNKS = BN / CHUNK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *ring = smem;
+    uint8_t *bres = ring + STAGES * STAGE_BYTES;
+    uint8_t *outbuf = bres + (kResident ? RES_BYTES : 0);
+    uint8_t *ones = outbuf + OUT_BYTES;
+    float *biasbuf = reinterpret_cast<float *>(ones + ONES_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(biasbuf) + BIAS_BYTES);
+    uint64_t *full = bars;                  // [STAGES] operands landed
+    uint64_t *empty = bars + STAGES;        // [STAGES] MMAs reading the stage are done
+    uint64_t *bfull = bars + 2 * STAGES;    // the resident slab landed
+    uint64_t *tfull = bfull + 1;            // [2] accumulator complete
+    uint64_t *tempty = tfull + 2;           // [2] accumulator drained (EPI_WARPS arrivals)
+    uint64_t *efull = tempty + 2;           // [EPI_WARPS][2] E block landed
+    uint64_t *drain = efull + 2 * EPI_WARPS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KernelCtl &ctl = args.ctl;
+    const bool with_ones = MODE == LIN_WG && args.sums != nullptr;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(bfull, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], EPI_WARPS);
+        }
+        for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(&efull[i], 1);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmY);
+        if (MODE != LIN_WG && args.has_e) tma_prefetch_desc(&tmE);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (with_ones) {
+        for (int i = threadIdx.x; i < ONES_BYTES / 4; i += THREADS) reinterpret_cast<uint32_t *>(ones)[i] = 0x3F803F80u;
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer ----------------
+            uint32_t issued = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            auto load_b = [&](uint8_t *dst, uint64_t *bar, int k0, int n0) {
+                if (!args.b_mn) {
+                    tma_load_3d(dst, &tmB, bar, k0, n0, 0);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < BN / 64; ++h) tma_load_3d(dst + h * (BK * 128), &tmB, bar, n0 + 64 * h, k0, 0);
+                }
+            };
+            if (kResident) {
+                const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
+                mbar_arrive_expect_tx(bfull, (uint32_t)(args.kblocks * B_BYTES));
+                for (int kb = 0; kb < args.kblocks; ++kb) load_b(bres + kb * B_BYTES, bfull, kb * BK, n0);
+            }
+            Tiles<MODE> t(args);
+            while (ok && t.next()) {
+                const int m0 = t.rt * BM, n0 = t.ct * BN;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl, SITE_LIN | 2, t.rt)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = ring + stage * STAGE_BYTES;
+                    mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+                    const int k0 = kb * BK;
+                    if (!args.a_mn) {
+                        tma_load_3d(sa, &tmA, &full[stage], k0, m0, 0);
+                    } else {
+                        tma_load_3d(sa, &tmA, &full[stage], m0, k0, 0);
+                        tma_load_3d(sa + BK * 128, &tmA, &full[stage], m0 + 64, k0, 0);
+                    }
+                    if (!kResident) load_b(sa + A_BYTES, &full[stage], k0, n0);
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // No copy may be in flight when the CTA leaves.
+            for (int s = 0; s < STAGES; ++s) {
+                const uint32_t n = issued / STAGES + ((uint32_t)s < issued % STAGES ? 1u : 0u);
+                if (n > 0) wait_drain(&full[s], (n - 1) & 1u, ctl.timeout_ns);
+            }
+            if (kResident) wait_drain(bfull, 0, ctl.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer ----------------
+            const uint32_t idesc = idesc_bf16(BM, BN, args.a_mn, args.b_mn);
+            const uint32_t idesc_ones = idesc_bf16(BM, 16, args.a_mn, 0);
+            int stage = 0, lt = 0;
+            uint32_t phase = 0;
+            bool ok = !kResident || wait_bounded(bfull, 0, abort_flag, ctl, SITE_LIN | 3, 0);
+            Tiles<MODE> t(args);
+            while (ok && t.next()) {
+                const int acc = lt & 1;
+                if (!wait_bounded(&tempty[acc], ((uint32_t)(lt >> 1) & 1u) ^ 1u, abort_flag, ctl, SITE_LIN | 4, t.rt)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * BN);
+                const bool sum_rows = with_ones && t.ct == 0;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!wait_bounded(&full[stage], phase, abort_flag, ctl, SITE_LIN | 5, t.rt)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + stage * STAGE_BYTES);
+                    const uint32_t sb = kResident ? smem_u32(bres + kb * B_BYTES) : sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        const uint64_t ad = args.a_mn ? sdesc_sw128(sa + kk * 2048, BK * 128, 1024)
+                                                      : sdesc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = args.b_mn ? sdesc_sw128(sb + kk * 2048, BK * 128, 1024)
+                                                      : sdesc_sw128(sb + kk * 32, 16, 1024);
+                        const uint32_t more = (kb != t.kb0 || kk != 0) ? 1u : 0u;
+                        mma_bf16(d, ad, bd, idesc, more);
+                        if (sum_rows)
+                            mma_bf16(tmem + ONES_COL + 16 * acc, ad, sdesc_sw128(smem_u32(ones) + kk * 32, 16, 1024),
+                                     idesc_ones, more);
+                    }
+                    mma_commit(&empty[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&tfull[acc]);
+                ++lt;
+            }
+            mma_commit(drain);
+            wait_drain(drain, 0, ctl.timeout_ns);
+        }
+    } else {
+        // ---------------- drain warps 2..9 ----------------
+        // Warp (q, h): accumulator rows 32 q .. 32 q + 31, chunks h, h + 2, ... of each tile. Block
+        // n of this warp (counted over all its tiles) goes through buffer n & 1.
+        const int ew = warp - 2, q = warp & 3, h = ew >> 2;
+        uint8_t *wbuf = outbuf + ew * 2 * WBUF;
+        uint64_t *ebar = efull + 2 * ew;
+        float *mybias = biasbuf + ew * 128;
+        const uint32_t lanebase = tmem + ((uint32_t)(q * 32) << 16);
+        const bool has_e = MODE != LIN_WG && args.has_e;
+        constexpr int MINE = (CHUNKS + 1) / 2;  // chunks of a tile that are this warp's (at most)
+        float colsum[2 * MINE];
+        int nst = 0, nload = 0, lt = 0;
+
+        // Iterator over this warp's blocks, for the E loads that run one block ahead.
+        Tiles<MODE> ahead(args);
+        int ahead_c = CHUNKS;
+        bool ahead_ok = has_e;
+        auto load_next_e = [&]() {
+            if (!ahead_ok) return;
+            for (;;) {
+                ahead_c += 2;
+                if (ahead_c >= CHUNKS) {
+                    if (!ahead.next()) {
+                        ahead_ok = false;
+                        return;
+                    }
+                    ahead_c = h;
+                    if (ahead_c >= CHUNKS) continue;
+                }
+                const int col = ahead.ct * BN + ahead_c * CHUNK, row = ahead.rt * BM + 32 * q;
+                if (col < args.N && row < args.M) {
+                    if (lane == 0) {
+                        tma_store_wait_read<0>();  // the block that last left from this buffer has been read
+                        mbar_arrive_expect_tx(&ebar[nload & 1], WBUF);
+                        tma_load_3d(wbuf + (nload & 1) * WBUF, &tmE, &ebar[nload & 1], col, row, 0);
+                    }
+                    ++nload;
+                    return;
+                }
+            }
+        };
+        load_next_e();
+        if (MODE != LIN_WG) {
+            const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
+            for (int i = lane; i < 64 * MINE; i += 32) {
+                const int col = n0 + (h + 2 * (i >> 6)) * 64 + (i & 63);
+                mybias[i] = (args.bias && col < args.N) ? __bfloat162float(args.bias[col]) : 0.f;
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * MINE; ++i) colsum[i] = 0.f;
+        bool ok = true;
+        Tiles<MODE> t(args);
+        while (ok && t.next()) {
+            const int acc = lt & 1;
+            if (!warp_wait(&tfull[acc], (uint32_t)(lt >> 1) & 1u, abort_flag, ctl, SITE_LIN | 6, t.rt)) break;
+            tc_fence_after();
+            const int row0 = t.rt * BM + 32 * q;
+#pragma unroll
+            for (int ci = 0; ci < MINE; ++ci) {
+                const int ch = h + 2 * ci, col = t.ct * BN + ch * CHUNK;
+                if (ch >= CHUNKS || row0 >= args.M || col >= args.N) continue;
+                uint8_t *ob = wbuf + (nst & 1) * WBUF;
+                const uint32_t taddr = lanebase + (uint32_t)(acc * BN + ch * CHUNK);
+                if constexpr (MODE == LIN_WG) {
+                    uint32_t v[32];
+                    tmem_ld32(taddr, v);
+                    if (lane == 0) tma_store_wait_read<1>();
+                    __syncwarp();
+                    tmem_ld_wait_regs(v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(ob + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                } else {
+                    uint32_t v[64];
+                    tmem_ld32(taddr, v);
+                    tmem_ld32(taddr + 32, v + 32);
+                    if (has_e) {
+                        load_next_e();
+                        if (!(ok = warp_wait(&ebar[nst & 1], (uint32_t)(nst >> 1) & 1u, abort_flag, ctl, SITE_LIN | 7, t.rt)))
+                            break;
+                    } else if (lane == 0) {
+                        tma_store_wait_read<1>();
+                    }
+                    __syncwarp();
+                    tmem_ld_wait_regs(v);
+                    finish<MODE>(args.act, v, mybias + ci * 64, has_e, ob + lane * 128, lane & 7);
+                    if constexpr (MODE == LIN_GRAD) {
+                        if (args.sums != nullptr) {
+                            colsum[2 * ci] += column_sum32(v, lane);
+                            colsum[2 * ci + 1] += column_sum32(v + 32, lane);
+                        }
+                    }
+                }
+                ++nst;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tmY, ob, col, row0, MODE == LIN_WG ? t.split : 0);
+                    tma_store_commit();
+                }
+            }
+            if (!ok) break;
+            if (with_ones && t.ct == 0 && h == 0) {
+                uint32_t v[16];
+                tmem_ld16(lanebase + (uint32_t)(ONES_COL + 16 * acc), v);
+                tmem_ld_wait_regs(v);
+                const int row = row0 + lane;
+                if (row < args.M) args.sums[(size_t)t.split * args.M + row] = __uint_as_float(v[0]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[acc]);
+            ++lt;
+        }
+        if (MODE == LIN_GRAD && args.sums != nullptr) {
+            float *dst = args.sums + (size_t)(((int)blockIdx.x / args.col_tiles) * 4 + q) * args.N;
+#pragma unroll
+            for (int i = 0; i < 2 * MINE; ++i) {
+                const int ch = h + 2 * (i >> 1), col = ((int)blockIdx.x % args.col_tiles) * BN + ch * 64 + 32 * (i & 1) + lane;
+                if (ch < CHUNKS && col < args.N) dst[col] = colsum[i];
+            }
+        }
+        // E blocks still in flight (only after a timeout: a complete pass consumed them all).
+        for (int n = nst; n < nload; ++n) wait_drain(&ebar[n & 1], (uint32_t)(n >> 1) & 1u, ctl.timeout_ns);
+        if (lane == 0) tma_store_wait_all<0>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// Sums of the split products and of the column-sum partials, rounded once to bf16.
+// dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. Each thread adds its element's
+// partials in order, so the result does not depend on the launch.
+// ---------------------------------------------------------------------------
+namespace {
+
+__global__ void __launch_bounds__(256) linear_reduce_kernel(const LinearReduceArgs a) {
+    const long long quads = a.count >> 2;  // n k is a multiple of 64
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i < quads && a.dw) {
+        const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < a.splits; ++k) {
+            const float4 v = __ldcs(p + (size_t)k * quads);
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+    // Bias gradient: one warp per 32 columns in the blocks after the weight's.
+    const long long j = i - (long long)a.weight_blocks * 256;
+    if (j >= 0 && j < a.n && a.db) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < a.sum_rows; ++k) s += a.sums[(size_t)k * a.n + j];
+        a.db[j] = __float2bfloat16_rn(s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s) {
+    a.weight_blocks = a.dw ? (int)((a.count / 4 + 255) / 256) : 0;
+    const int grid = a.weight_blocks + (a.db ? (a.n + 255) / 256 : 0);
+    if (grid == 0) return cudaSuccess;
+    linear_reduce_kernel<<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+namespace {
+template <int BN, bool RES, int MODE>
+cudaError_t allow() {
+    return cudaFuncSetAttribute(linear_tc_kernel<BN, RES, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)lin::smem(BN, RES));
+}
+template <int BN, bool RES, int MODE>
+void go(const LinearMaps &m, const LinearArgs &a, int grid, cudaStream_t s) {
+    linear_tc_kernel<BN, RES, MODE><<<grid, lin::THREADS, lin::smem(BN, RES), s>>>(m.a, m.b, m.e, m.y, a);
+}
+template <int MODE>
+void pick(const LinearMaps &m, const LinearArgs &a, int bn, bool res, int grid, cudaStream_t s) {
+    if (bn == 64) res ? go<64, true, MODE>(m, a, grid, s) : go<64, false, MODE>(m, a, grid, s);
+    else if (bn == 128) res ? go<128, true, MODE>(m, a, grid, s) : go<128, false, MODE>(m, a, grid, s);
+    else res ? go<256, true, MODE>(m, a, grid, s) : go<256, false, MODE>(m, a, grid, s);
+}
+}  // namespace
+
+bool linear_resident(int bn, int kblocks) { return (long long)kblocks * bn * lin::BK * 2 <= lin::RES_BYTES; }
+
+cudaError_t linear_tc_setup() {
+    cudaError_t e;
+    if ((e = allow<64, true, LIN_FWD>()) || (e = allow<64, false, LIN_FWD>()) || (e = allow<128, true, LIN_FWD>()) ||
+        (e = allow<128, false, LIN_FWD>()) || (e = allow<256, true, LIN_FWD>()) || (e = allow<256, false, LIN_FWD>()) ||
+        (e = allow<64, true, LIN_GRAD>()) || (e = allow<64, false, LIN_GRAD>()) || (e = allow<128, true, LIN_GRAD>()) ||
+        (e = allow<128, false, LIN_GRAD>()) || (e = allow<256, true, LIN_GRAD>()) ||
+        (e = allow<256, false, LIN_GRAD>()))
+        return e;
+    return allow<128, false, LIN_WG>();
+}
+
+cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, cudaStream_t s) {
+    if (mode == LIN_WG) go<128, false, LIN_WG>(m, a, grid, s);
+    else if (mode == LIN_GRAD) pick<LIN_GRAD>(m, a, bn, linear_resident(bn, a.kblocks), grid, s);
+    else pick<LIN_FWD>(m, a, bn, linear_resident(bn, a.kblocks), grid, s);
+    return cudaGetLastError();
+}
+
+}  // namespace trimul

@@ -1,0 +1,268 @@
+"""GPU parity of the linear layer and its gradients (trimul_linear_forward / backward, through the
+C ABI) against the float64 oracle (oracle/linear.py).
+
+Tolerances, per element. u = 2^-8 is the largest relative error of one rounding to bf16, e = 2^-23
+that of an fp32 operation (the tensor core's sums may truncate). A sum of K products kept in fp32
+is off by at most (K + 4) e times the sum of their sizes S.
+  forward   p is off by dp = (K + 4) e (S + |b|); an activation's slope is at most 1.1 and its own
+            evaluation (hardware exponential and reciprocal, about 2^-21) 2^-19 of its size;
+            the residual's addition adds e |r|; then one rounding: u |y|.
+  D         dy act'(p): act' has slope at most 1 (0 for identity; relu's inputs here are on a grid
+            where p is exact), so D is off by |dy| (dp + 2^-18); rounding D to bf16 adds u |D| for
+            sigmoid and silu only.
+  dx, dW    sums of these: the D errors times the other factor, summed, plus (K + 4) e of the sizes,
+            plus the final rounding.
+  db        sums D before its rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import pair_representation_b200 as tm
+from gpu_helpers import as_bf16
+from oracle.linear import linear as oracle_linear, linear_backward as oracle_backward
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+U, E = 2.0 ** -8, 2.0 ** -23
+ACTS = ("none", "relu", "sigmoid", "silu")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from pair_representation_b200 import build
+    build.build()
+    tm.lib()
+
+
+def draw(rows, k, n, seed, grid=False):
+    rng = np.random.default_rng([rows, k, n, seed])
+    if grid:  # multiples of 1/4 and 1/8: every product and sum is exact, p = 0 included
+        x = rng.integers(-8, 9, size=(rows, k)) / 4
+        w = rng.integers(-8, 9, size=(n, k)) / 8
+        b = rng.integers(-8, 9, size=n) / 8
+    else:
+        x = rng.standard_normal((rows, k)) * rng.uniform(0.5, 2, size=k)
+        w = rng.standard_normal((n, k)) / np.sqrt(k)
+        b = rng.standard_normal(n)
+    return [as_bf16(t) for t in (x, w, b, rng.standard_normal((rows, n)))]
+
+
+def dev(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(DEV).to(torch.bfloat16)
+
+
+def within(got, ref, tol):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    over = np.abs(got - ref) - tol
+    assert over.max() <= 0, float(over.max())
+
+
+def check_forward(rows, k, n, act, bias, residual, seed=0):
+    x, w, b, r = draw(rows, k, n, seed)
+    b, r = (b if bias else None), (r if residual else None)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    y = tm.linear(dev(x), dev(w), bias=dev(b), residual=dev(r), act=act, workspace=ws)
+    rc, detail = tm.device_status(ws)
+    assert rc == 0, (rc, detail)
+    ref = oracle_linear(x, w, b, r, act)
+    size = np.abs(x).astype(np.float64) @ np.abs(w).astype(np.float64).T + (0 if b is None else np.abs(b))
+    inner = ref if r is None else ref - r
+    within(y, ref, U * np.abs(ref) + 1.1 * (k + 4) * E * size + 2.0 ** -19 * np.abs(inner) +
+           (0 if r is None else E * np.abs(r)))
+
+
+SIZES = [(1, 8, 8), (1, 128, 128), (2, 40, 16), (31, 64, 64), (33, 72, 56), (127, 128, 128), (128, 136, 120),
+         (129, 256, 264), (257, 320, 512), (300, 512, 128), (1000, 200, 328), (64, 1024, 1024), (2500, 128, 512)]
+
+
+@pytest.mark.parametrize("rows,k,n", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_forward(rows, k, n, act):
+    odd = (rows + k) % 3
+    check_forward(rows, k, n, act, bias=odd != 0, residual=odd != 1)
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("residual", [True, False])
+def test_forward_many_rows(bias, residual):
+    """More row tiles than SMs: every CTA goes round its ring, its accumulators and its buffers."""
+    check_forward(148 * 128 * 2 + 77, 72, 72, "silu", bias, residual)
+    check_forward(148 * 128 + 1, 128, 264, "sigmoid", bias, residual)
+
+
+def test_forward_widest():
+    check_forward(200, 64, 10944, "relu", True, True)
+    check_forward(130, 72, 16384, "none", True, False)
+    check_forward(3, 16384, 40, "none", True, False)
+
+
+def check_backward(rows, k, n, act, bias=True, held=False, seed=1):
+    x, w, b, dy = draw(rows, k, n, seed, grid=act == "relu")
+    b = b if bias else None
+    xt = dev(x)
+    if held:
+        a = tm.act8_pack(xt)
+        x = tm.act8_unpack(a).float().cpu().numpy()
+        if act == "relu":  # 8 bits hold these multiples of 1/4 exactly
+            assert np.array_equal(x, xt.float().cpu().numpy())
+        xt = a
+    need = tm.trimul_linear_backward_workspace_size(rows, k, n, tm.ACTS[act], held)
+    ws = torch.full((need,), 0x5A, dtype=torch.uint8, device=DEV)
+    dx, dw, db = tm.linear_backward(xt, dev(w), dev(dy), bias=dev(b), act=act, workspace=ws)
+    rc, detail = tm.device_status(ws)
+    assert rc == 0, (rc, detail)
+    rx, rw, rb, D = oracle_backward(x, w, dy, b, act)
+    ax, aw, ay, aD = (np.abs(np.asarray(t, np.float64)) for t in (x, w, dy, D))
+    smooth = act in ("sigmoid", "silu")
+    dD = ay * ((k + 4) * E * (ax @ aw.T + (0 if b is None else np.abs(b))) + 2.0 ** -18) if smooth else np.zeros_like(aD)
+    dDr = dD + (U * (aD + dD) if smooth else 0)
+    within(dx, rx, U * np.abs(rx) + 1.01 * (dDr @ aw + (n + 4) * E * (aD @ aw)))
+    within(dw, rw, U * np.abs(rw) + 1.01 * (dDr.T @ ax + (rows + 4) * E * (aD.T @ ax)))
+    within(db, rb, U * np.abs(rb) + 1.01 * (dD.sum(0) + (rows + 4) * E * aD.sum(0)))
+    # As whole arrays: the roundings are of random sign, so two of them stay under 1.5 u.
+    for got, ref in ((dx, rx), (dw, rw)):
+        if ref.size > 64 and np.linalg.norm(ref):
+            assert np.linalg.norm(got.double().cpu().numpy() - ref) <= 1.5 * U * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("rows,k,n", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_backward(rows, k, n, act):
+    check_backward(rows, k, n, act, bias=(rows + n) % 3 != 0)
+
+
+@pytest.mark.parametrize("rows,k,n", [(1, 32, 8), (5, 64, 24), (129, 96, 136), (1000, 128, 512), (700, 512, 128),
+                                      (333, 128, 128)])
+@pytest.mark.parametrize("act", ACTS)
+def test_backward_from_8_bits(rows, k, n, act):
+    check_backward(rows, k, n, act, held=True)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("held", [True, False])
+def test_backward_many_rows(act, held):
+    check_backward(148 * 128 + 77, 128, 128, act, held=held)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_parts_of_the_backward(act):
+    """Each gradient alone equals the one of the whole call, bit for bit."""
+    x, w, b, dy = (dev(t) for t in draw(500, 96, 160, 2))
+    for xx in (x, tm.act8_pack(x)):
+        full = tm.linear_backward(xx, w, dy, bias=b, act=act)
+        for i in range(3):
+            part = tm.linear_backward(xx, w, dy, bias=b, act=act, need_dx=i == 0, need_dw=i == 1, need_db=i == 2)
+            assert [t is None for t in part] == [j != i for j in range(3)]
+            assert torch.equal(part[i], full[i])
+        assert tm.linear_backward(xx, w, dy, act=act, need_dx=False, need_dw=False, need_db=False) == (None,) * 3
+
+
+def test_equal_calls_give_equal_bits():
+    x, w, b, dy = (dev(t) for t in draw(20000, 128, 256, 3))
+    for act in ("none", "sigmoid"):
+        first = tm.linear_backward(x, w, dy, bias=b, act=act)
+        for _ in range(3):
+            assert all(torch.equal(p, q) for p, q in zip(first, tm.linear_backward(x, w, dy, bias=b, act=act)))
+
+
+def test_infinities_and_nan():
+    """A NaN in a row of x reaches that row of y alone; large and infinite pre-activations end at the
+    activation's limits."""
+    x, w, b, _ = draw(300, 64, 64, 4)
+    x[17, 3] = np.nan
+    for act in ACTS:
+        y = tm.linear(dev(x), dev(w), bias=dev(b), act=act).float().cpu().numpy()
+        assert np.isnan(y[17]).all() and np.isfinite(np.delete(y, 17, 0)).all(), act
+    p = np.array([-3e38, -1e5, -200, -90, -80, 0, 80, 200, 1e5, 3e38], np.float32)
+    x = np.zeros((len(p), 8), np.float32)
+    x[:, 0] = as_bf16(p)
+    w = np.eye(8, dtype=np.float32)
+    with np.errstate(over="ignore"):
+        for act in ACTS:
+            y = tm.linear(dev(x), dev(w), act=act).double().cpu().numpy()
+            ref = oracle_linear(x, w, act_name=act)
+            assert np.isfinite(y).all()
+            assert (np.abs(y - ref) <= U * np.abs(ref) + 1e-34).all(), act
+            dx, _, _ = tm.linear_backward(dev(x), dev(w), dev(np.ones((len(p), 8))), act=act)
+            rx = oracle_backward(x, w, np.ones((len(p), 8)), act_name=act)[0]
+            assert (np.abs(dx.double().cpu().numpy() - rx) <= 2.1 * U * np.abs(rx) + 1e-34).all(), act
+
+
+def test_residual_in_place():
+    x, w, b, r = (dev(t) for t in draw(1500, 128, 200, 5))
+    ref = tm.linear(x, w, bias=b, residual=r, act="silu")
+    got = tm.linear(x, w, bias=b, residual=r, act="silu", out=r)
+    assert got is r and torch.equal(got, ref)
+
+
+def test_nothing_around_the_outputs_is_written():
+    rows, k, n = 77, 72, 136
+    x, w, b, dy = (dev(t) for t in draw(rows, k, n, 6))
+
+    def frame(count):
+        t = torch.full((count + 256,), 7.0, dtype=torch.bfloat16, device=DEV)
+        return t, t[128:128 + count]
+
+    (fy, y), (fx, dx), (fw, dw), (fb, db) = (frame(c) for c in (rows * n, rows * k, n * k, n))
+    need = tm.trimul_linear_backward_workspace_size(rows, k, n, 3)
+    fws = torch.full((need + 256,), 9, dtype=torch.uint8, device=DEV)
+    p = tm.LinearParams(rows, k, n, 3, w.data_ptr(), b.data_ptr(), fws.data_ptr(), need, 0)
+    tm.trimul_linear_forward(x, None, p, y)
+    tm.trimul_linear_backward(x, None, dy, p, dx, dw, db)
+    torch.cuda.synchronize()
+    for f, v in ((fy, y), (fx, dx), (fw, dw), (fb, db)):
+        assert (f[:128] == 7).all() and (f[128 + v.numel():] == 7).all()
+    assert (fws[need:] == 9).all()
+    assert torch.equal(y.view(rows, n), tm.linear(x, w, bias=b, act="silu"))
+    for v, t in zip((dx, dw, db), tm.linear_backward(x, w, dy, bias=b, act="silu")):
+        assert torch.equal(v.view(t.shape), t)
+
+
+def test_leading_dimensions_empty_batches_streams_and_graphs():
+    x, w, b, dy = (dev(t) for t in draw(240, 64, 96, 7))
+    y = tm.linear(x, w, bias=b, act="sigmoid")
+    assert torch.equal(tm.linear(x.view(4, 5, 12, 64), w, bias=b, act="sigmoid"), y.view(4, 5, 12, 96))
+    grads = tm.linear_backward(x, w, dy, bias=b, act="sigmoid")
+    got = tm.linear_backward(x.view(4, 60, 64), w, dy.view(4, 60, 96), bias=b, act="sigmoid")
+    assert got[0].shape == (4, 60, 64) and all(torch.equal(p.reshape(-1), q.reshape(-1)) for p, q in zip(got, grads))
+    assert tm.linear(x[:0], w).shape == (0, 96)
+    dx, dw, db = tm.linear_backward(x[:0], w, dy[:0])
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = tm.linear_backward(x, w, dy, bias=b, act="sigmoid", stream=side)
+    y2 = tm.linear(x, w, bias=b, act="sigmoid", stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(y2, y) and all(torch.equal(p, q) for p, q in zip(got, grads))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y3 = tm.linear(x, w, bias=b, act="sigmoid")
+        got = tm.linear_backward(x, w, dy, bias=b, act="sigmoid")
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y3, y) and all(torch.equal(p, q) for p, q in zip(got, grads))
+
+
+def test_refusals():
+    x, w, b, dy = (dev(t) for t in draw(10, 64, 32, 8))
+    bad = [lambda: tm.linear(x.float(), w), lambda: tm.linear(x.t(), w), lambda: tm.linear(x, w.t()),
+           lambda: tm.linear(x, w, bias=b[:8]), lambda: tm.linear(x, w, act="tanh"),
+           lambda: tm.linear(x, w, residual=dy[:5]), lambda: tm.linear(x, w, out=dy[:5]),
+           lambda: tm.linear(x.cpu(), w), lambda: tm.linear_backward(x, w, x), lambda: tm.linear_backward(x[:5], w, dy),
+           lambda: tm.linear_backward(tm.act8_pack(x[:, :32].contiguous()), w, dy), lambda: tm.act8_pack(x[:, :40]),
+           lambda: tm.act8_pack(x[:, :40].contiguous())]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    small = torch.zeros(128, dtype=torch.uint8, device=DEV)
+    for f in (lambda: tm.linear(x, w, workspace=small), lambda: tm.linear_backward(x, w, dy, workspace=small),
+              lambda: tm.linear(x[:, :60].contiguous(), w[:, :60].contiguous()),
+              lambda: tm.linear(dy, dev(np.eye(32)), out=dy)):
+        with pytest.raises(tm.TrimulError):
+            f()
