@@ -436,64 +436,101 @@ def atomattn_backward(params: AtomAttnParams, dout, grads: AtomAttnGrads, stream
     return rc
 
 
-def _bf16(what: str, like, *tensors):
-    """Every tensor (None passes) must be contiguous bf16 on `like`'s CUDA device."""
+def _need_bf16(what: str, index: int, *tensors):
+    """Every tensor (None passes) must be contiguous bf16 on CUDA device `index`."""
     import torch
-    for t in (like,) + tensors:
+    if index < 0:
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    bf16 = torch.bfloat16
+    for t in tensors:
         if t is None:
             continue
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype is not bf16 or not t.is_contiguous():
             raise ValueError(f"{what}: tensors must be contiguous bf16")
-        if t.device != like.device or t.device.type != "cuda":
+        if t.get_device() != index:
             raise ValueError(f"{what}: tensors must be on one CUDA device")
 
 
-def _call_on(device, stream, inputs, call):
-    """``call(stream handle)`` with `device` current and, where a stream is given, that stream
-    current too, so that what the call allocates belongs to it. Inputs of other streams are
-    marked as used there: their memory is not handed out again before this work is done."""
+def _need_workspace(what: str, index: int, workspace):
     import torch
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-    with torch.cuda.device(device), torch.cuda.stream(s):
-        out = call(s.cuda_stream)
-        for t in inputs:
-            if t is not None:
-                t.record_stream(s)
-        return out
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
+                                  or workspace.get_device() != index):
+        raise ValueError(f"{what}: workspace must be contiguous uint8 on the tensors' device")
+
+
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call must change the current device or stream first."""
+    import torch
+    return stream is not None or torch.cuda.current_device() != index
+
+
+def _run_on(index: int, stream, tensors, call):
+    """call() with device `index` current and, where one is given, `stream` current too, so that
+    what the call allocates belongs to it. `tensors` may be another stream's: they are marked as
+    used on this one, so that their memory is not handed out again before this work is done."""
+    import torch
+    with torch.cuda.device(index):
+        if stream is None:
+            return call()
+        s = torch.cuda.ExternalStream(stream, device=index) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            out = call()
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+            return out
+
+
+def _raw_stream(index: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+_status = {}  # device index -> status workspace of the calls that are given none
+
+
+def _status_workspace(like):
+    """256 bytes for the status word of a call that the caller gave no workspace: one buffer per
+    device, kept. Calls that overlap share it, which only their status notices. A first call
+    inside a capture takes memory of the graph's own instead."""
+    import torch
+    ws = _status.get(like.get_device())
+    if ws is None:
+        ws = torch.zeros(256, dtype=torch.uint8, device=like.device)
+        if not torch.cuda.is_current_stream_capturing():
+            _status[like.get_device()] = ws
+    return ws
 
 
 def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=None, stream=None):
     """Gradients of sum(atom_attention(q, k, v, bias, atom_mask) * dout) (include/atomattn.h).
 
     Arguments as for atom_attention, dout like q. Returns (dq, dk, dv, dbias), dbias None
-    without bias. A caller that gives `workspace` (atomattn_workspace_size() bytes) can read
-    the call's status there (device_status)."""
+    without bias. `workspace` (atomattn_workspace_size() bytes): where device_status finds this
+    call's status; without one, calls of a device share a status word."""
     import torch
-    if q.dim() != 4 or q.shape[-1] != 32 or k.shape != q.shape or v.shape != q.shape or dout.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != 32 or k.shape != shape or v.shape != shape or dout.shape != shape:
         raise ValueError("q, k, v, dout must be [batch, n_atoms, heads, 32] of one shape")
-    B, n, H, _ = q.shape
+    B, n, H, _ = shape
     if bias is not None and tuple(bias.shape) != (B, (n + 31) // 32, H, 32, 128):
         raise ValueError("bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
     if atom_mask is not None and tuple(atom_mask.shape) != (B, n):
         raise ValueError("atom_mask must be [batch, n_atoms]")
-    _bf16("atom_attention_backward", q, k, v, dout, bias, atom_mask)
-
-    def call(s):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
-        dbias = None if bias is None else torch.empty_like(bias)
-        ws = workspace if workspace is not None else torch.empty(atomattn_workspace_size(), dtype=torch.uint8,
-                                                                 device=q.device)
-        p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask),
-                           ws.data_ptr(), ws.numel(), 0)
-        atomattn_backward(p, dout, AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias)), s)
-        return dq, dk, dv, dbias
-
-    return _call_on(q.device, stream, (q, k, v, dout, bias, atom_mask, workspace), call)
+    index = q.get_device()
+    _need_bf16("atom_attention_backward", index, q, k, v, dout, bias, atom_mask)
+    _need_workspace("atom_attention_backward", index, workspace)
+    if _elsewhere(index, stream):
+        return _run_on(index, stream, (q, k, v, dout, bias, atom_mask, workspace),
+                       lambda: atom_attention_backward(q, k, v, dout, bias, atom_mask, workspace))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dbias = None if bias is None else torch.empty_like(bias)
+    ws = _status_workspace(q) if workspace is None else workspace
+    p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask),
+                       ws.data_ptr(), ws.numel(), 0)
+    atomattn_backward(p, dout, AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias)),
+                      _raw_stream(index))
+    return dq, dk, dv, dbias
 
 
 # ---- linear layers and activations in 8 bits (include/linear.h) -----------------
@@ -544,11 +581,19 @@ def trimul_act8_unpack(codes, scales, rows: int, channels: int, x, stream=None, 
 
 
 def device_status(workspace, stream=None):
-    """(code, [code, site, block, aux]) that the last call with this workspace left (synchronises):
-    linear, linear_backward or atom_attention_backward."""
+    """(code, [code, site, block, aux]) that the last linear, linear_backward or
+    atom_attention_backward call with this workspace left (synchronises); with a device in the
+    workspace's place, the last such call of that device that was given none."""
+    import torch
+    if not isinstance(workspace, torch.Tensor):
+        device = torch.device(workspace)
+        index = torch.cuda.current_device() if device.index is None else device.index
+        if index not in _status:
+            return 0, [0, 0, 0, 0]
+        workspace = _status[index]
     p = LinearParams()
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    return _call_on(workspace.device, stream, (), lambda s: trimul_linear_device_status(p, s))
+    return _run_on(workspace.get_device(), stream, (), lambda: trimul_linear_device_status(p))
 
 
 class Act8:
@@ -560,11 +605,11 @@ class Act8:
 
     def __init__(self, codes, scales):
         import torch
-        if codes.dim() < 1 or codes.shape[-1] % 32 or codes.shape[-1] == 0 or \
-                scales.shape != codes.shape[:-1] + (codes.shape[-1] // 32,):
+        shape, c = codes.shape, codes.shape[-1] if codes.dim() else 0
+        if c == 0 or c % 32 or scales.shape != shape[:-1] + (c // 32,):
             raise ValueError("codes must be [..., channels] and scales [..., channels / 32]")
         for t in (codes, scales):
-            if t.dtype != torch.uint8 or not t.is_contiguous():
+            if t.dtype is not torch.uint8 or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous uint8")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
@@ -582,49 +627,48 @@ class Act8:
 def act8_pack(x, stream=None) -> Act8:
     """Keep a bf16 tensor [..., channels] (channels a multiple of 32) in 33/32 bytes per value."""
     import torch
-    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % 32:
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] == 0 or shape[-1] % 32:
         raise ValueError("x must be [..., channels], channels a multiple of 32")
-    _bf16("act8_pack", x)
-    c = x.shape[-1]
-
-    def call(s):
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(x.shape[:-1] + (c // 32,), dtype=torch.uint8, device=x.device)
-        if x.numel():
-            trimul_act8_pack(x, x.numel() // c, c, codes, scales, s)
-        return Act8(codes, scales)
-
-    return _call_on(x.device, stream, (x,), call)
+    index = x.get_device()
+    _need_bf16("act8_pack", index, x)
+    if _elsewhere(index, stream):
+        return _run_on(index, stream, (x,), lambda: act8_pack(x))
+    c = shape[-1]
+    codes = torch.empty_like(x, dtype=torch.uint8)
+    scales = codes.new_empty(shape[:-1] + (c // 32,))
+    if codes.numel():
+        trimul_act8_pack(x, codes.numel() // c, c, codes, scales, _raw_stream(index))
+    return Act8(codes, scales)
 
 
 def act8_unpack(a: Act8, out=None, stream=None):
     """The values an Act8 stands for, as a bf16 tensor (written to `out` if given)."""
     import torch
-    c = a.shape[-1]
-    if a.device.type != "cuda":
-        raise ValueError("act8_unpack: codes and scales must be on a CUDA device")
-    if out is not None:
-        if out.shape != a.shape or out.device != a.device:
-            raise ValueError("out must have the codes' shape and device")
-        _bf16("act8_unpack", out)
-
-    def call(s):
-        x = out if out is not None else torch.empty(a.shape, dtype=torch.bfloat16, device=a.device)
-        if x.numel():
-            trimul_act8_unpack(a.codes, a.scales, x.numel() // c, c, x, s)
-        return x
-
-    return _call_on(a.device, stream, (a.codes, a.scales, out), call)
+    codes, scales = a.codes, a.scales
+    index = codes.get_device()
+    if out is not None and out.shape != codes.shape:
+        raise ValueError("out must have the codes' shape")
+    _need_bf16("act8_unpack", index, out)
+    if _elsewhere(index, stream):
+        return _run_on(index, stream, (codes, scales, out), lambda: act8_unpack(a, out))
+    x = torch.empty_like(codes, dtype=torch.bfloat16) if out is None else out
+    if x.numel():
+        c = codes.shape[-1]
+        trimul_act8_unpack(codes, scales, x.numel() // c, c, x, _raw_stream(index))
+    return x
 
 
-def _linear_shapes(what, x, weight, bias, act):
-    if weight.dim() != 2 or len(x.shape) < 1 or x.shape[-1] != weight.shape[1]:
+def _linear_shape(what, x_shape, weight, bias, act):
+    """Shape of the layer's result."""
+    w = weight.shape
+    if len(w) != 2 or len(x_shape) < 1 or x_shape[-1] != w[1]:
         raise ValueError(f"{what}: x must be [..., in_features] and weight [out_features, in_features]")
-    if bias is not None and tuple(bias.shape) != (weight.shape[0],):
+    if bias is not None and (bias.dim() != 1 or bias.shape[0] != w[0]):
         raise ValueError(f"{what}: bias must be [out_features]")
     if act not in ACTS:
         raise ValueError(f"{what}: act must be one of {', '.join(ACTS)}")
-    return tuple(x.shape[:-1]) + (weight.shape[0],)
+    return x_shape[:-1] + w[:1]
 
 
 def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=None, stream=None):
@@ -633,29 +677,27 @@ def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=
     x: [..., in_features]; weight: [out_features, in_features] (both multiples of 8); bias:
     [out_features] or None; residual: like the result, or None; act: "none", "relu",
     "sigmoid" or "silu". Returns out (allocated if None; it may be the residual itself). Not
-    recorded by autograd: linear_backward gives the gradients. A caller that gives
-    `workspace` (trimul_linear_workspace_size() bytes) can read the call's status there
-    (device_status)."""
-    import torch
-    shape = _linear_shapes("linear", x, weight, bias, act)
-    _bf16("linear", x, weight, bias, residual, out)
-    if residual is not None and tuple(residual.shape) != shape:
+    recorded by autograd: linear_backward gives the gradients. `workspace`
+    (trimul_linear_workspace_size() bytes): where device_status finds this call's status;
+    without one, calls of a device share a status word."""
+    shape = _linear_shape("linear", x.shape, weight, bias, act)
+    index = x.get_device()
+    _need_bf16("linear", index, x, weight, bias, residual, out)
+    _need_workspace("linear", index, workspace)
+    if residual is not None and residual.shape != shape:
         raise ValueError("linear: residual must have the result's shape")
-    if out is not None and tuple(out.shape) != shape:
+    if out is not None and out.shape != shape:
         raise ValueError("linear: out must have the result's shape")
-    n, k = weight.shape
-
-    def call(s):
-        y = out if out is not None else torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        if y.numel():
-            ws = workspace if workspace is not None else torch.empty(trimul_linear_workspace_size(), dtype=torch.uint8,
-                                                                     device=x.device)
-            p = LinearParams(y.numel() // n, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(),
-                             0)
-            trimul_linear_forward(x, residual, p, y, s)
-        return y
-
-    return _call_on(x.device, stream, (x, weight, bias, residual, out, workspace), call)
+    if _elsewhere(index, stream):
+        return _run_on(index, stream, (x, weight, bias, residual, out, workspace),
+                       lambda: linear(x, weight, bias, residual, act, out, workspace))
+    y = x.new_empty(shape) if out is None else out
+    if y.numel():
+        n, k = weight.shape
+        ws = _status_workspace(x) if workspace is None else workspace
+        p = LinearParams(y.numel() // n, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
+        trimul_linear_forward(x, residual, p, y, _raw_stream(index))
+    return y
 
 
 def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_dw=True, need_db=True, workspace=None,
@@ -665,38 +707,41 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
     x is the forward's input, or the Act8 that kept it. What is not needed is not computed
     and comes back as None; db is computed without bias too (a bias of zeros). The
     residual's gradient is dout itself. `workspace`: trimul_linear_backward_workspace_size
-    bytes, for callers that keep one or read the call's status from it (device_status)."""
+    bytes, for callers that keep one or want the call's status (device_status)."""
     import torch
     held = isinstance(x, Act8)
-    shape = _linear_shapes("linear_backward", x, weight, bias, act)
-    if tuple(dout.shape) != shape:
+    shape = _linear_shape("linear_backward", x.shape, weight, bias, act)
+    if dout.shape != shape:
         raise ValueError("linear_backward: dout must be [..., out_features] with x's leading dimensions")
-    _bf16("linear_backward", weight, None if held else x, dout, bias)
-    if x.device != weight.device:
+    index = weight.get_device()
+    _need_bf16("linear_backward", index, weight, None if held else x, dout, bias)
+    _need_workspace("linear_backward", index, workspace)
+    if held and x.codes.get_device() != index:
         raise ValueError("linear_backward: tensors must be on one CUDA device")
+    if _elsewhere(index, stream):
+        tensors = (x.codes, x.scales) if held else (x,)
+        return _run_on(index, stream, tensors + (weight, dout, bias, workspace),
+                       lambda: linear_backward(x, weight, dout, bias, act, need_dx, need_dw, need_db, workspace))
     n, k = weight.shape
-
-    def call(s):
-        new = lambda shape: torch.empty(shape, dtype=torch.bfloat16, device=weight.device)  # noqa: E731
-        dx = new(tuple(x.shape)) if need_dx else None
-        dw = new((n, k)) if need_dw else None
-        db = new((n,)) if need_db else None
-        rows = dout.numel() // n if n else 0
-        if rows == 0:  # nothing to sum over
-            for t in (dw, db):
-                if t is not None:
-                    t.zero_()
-            return dx, dw, db
-        need = trimul_linear_backward_workspace_size(rows, k, n, ACTS[act], held)
-        ws = workspace if workspace is not None else torch.empty(max(need, 256), dtype=torch.uint8,
-                                                                 device=weight.device)
-        p = LinearParams(rows, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
-        x8 = Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()) if held else None
-        trimul_linear_backward(None if held else x, x8, dout, p, dx, dw, db, s)
+    dx = None if not need_dx else torch.empty_like(x) if not held else weight.new_empty(x.shape)
+    dw = torch.empty_like(weight) if need_dw else None
+    db = None if not need_db else torch.empty_like(bias) if bias is not None else weight.new_empty(n)
+    rows = dout.numel() // n if n else 0
+    if rows == 0:  # nothing to sum over
+        for t in (dw, db):
+            if t is not None:
+                t.zero_()
         return dx, dw, db
-
-    tensors = (x.codes, x.scales) if held else (x,)
-    return _call_on(weight.device, stream, tensors + (weight, dout, bias, workspace), call)
+    code = ACTS[act]
+    ws = workspace if workspace is not None else torch.empty(
+        max(256, trimul_linear_backward_workspace_size(rows, k, n, code, held)), dtype=torch.uint8, device=weight.device)
+    p = LinearParams(rows, k, n, code, weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
+    if held:
+        trimul_linear_backward(None, Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()), dout, p, dx, dw, db,
+                               _raw_stream(index))
+    else:
+        trimul_linear_backward(x, None, dout, p, dx, dw, db, _raw_stream(index))
+    return dx, dw, db
 
 
 # ---- the layer as the pages use it ------------------------------------------

@@ -1287,6 +1287,9 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.act = act;
     a.has_e = E != nullptr;
     a.bias = static_cast<const __nv_bfloat16 *>(bias);
+    a.x = static_cast<const __nv_bfloat16 *>(A);
+    a.w = static_cast<const __nv_bfloat16 *>(B);
+    a.K = K;
     a.sums = sums;
     a.clear_status = clear ? 1 : 0;
     a.ctl = ctl;

@@ -301,6 +301,8 @@ struct LinearArgs {
     int splits, kb_per_split;  // LIN_WG: the contraction in `splits` parts
     int act, has_e;
     const __nv_bfloat16 *bias;  // [N] or null
+    const __nv_bfloat16 *x, *w; // LIN_GRAD: A and B again, [M][K] and [N][K]
+    int K;
     float *sums;  // LIN_GRAD: [groups * 4][N] column sums of Y; LIN_WG: [splits][M] row sums of A; or null
     int clear_status;
     KernelCtl ctl;

@@ -113,7 +113,6 @@ __device__ __forceinline__ float act_fwd(float p) {
 // both factors are still finite and every slope is under 2e-36.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float p, float d) {
-    if (ACT == LIN_RELU) return p > 0.f ? d : 0.f;
     if (ACT == LIN_NONE) return d;
     p = max_nan(p, -87.f);
     const float e = exp_neg(p), s = rcpf(1.f + e), c = s * e;
@@ -157,9 +156,62 @@ __device__ __forceinline__ void finish_row(uint32_t (&v)[64], const float *bias,
 template <int MODE>
 __device__ __forceinline__ void finish(int act, uint32_t (&v)[64], const float *bias, bool has_e, uint8_t *row, int x7) {
     if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(v, bias, has_e, row, x7);
-    else if (act == LIN_RELU) finish_row<MODE, LIN_RELU>(v, bias, has_e, row, x7);
+    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(v, bias, has_e, row, x7);
     else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(v, bias, has_e, row, x7);
     else finish_row<MODE, LIN_SILU>(v, bias, has_e, row, x7);
+}
+
+// relu's gradient of one accumulator row: keep E where p > 0. The accumulator's rounding decides
+// the sign of a p next to 0, and a wrong one is not a small error of the gradient but the
+// whole of dy: where |p| is under the bound of that rounding (one step of 2^-22 of the row's
+// largest sum for each 16 products), the warp takes the row's product again in 64 bits,
+// one place at a time. At random inputs about 1 in 10^5 places.
+__device__ __forceinline__ void finish_row_relu_grad(uint32_t (&v)[64], const float *bias, uint8_t *row, int x7,
+                                                     const LinearArgs &a, int r, int col0, int lane) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) top = fmaxf(top, fabsf(__uint_as_float(v[j])));
+    const float near_ = top * (float)(4 * a.kblocks + 8) * 2.384185791015625e-7f;
+    uint64_t keep = 0, check = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+        const float p = __uint_as_float(v[j]) + bias[j];
+        keep |= (uint64_t)(p > 0.f) << j;
+        check |= (uint64_t)(fabsf(p) < near_) << j;
+    }
+    if (r >= a.M) check = 0;
+    if (a.N - col0 < 64) check &= (1ull << (a.N - col0)) - 1;
+    for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
+        const int src = __ffs(who) - 1;
+        const __nv_bfloat16 *xr = a.x + (size_t)(r - lane + src) * a.K;
+        for (uint64_t left = __shfl_sync(0xffffffffu, check, src); left; left &= left - 1) {
+            const int j = __ffsll((long long)left) - 1;
+            const __nv_bfloat16 *wr = a.w + (size_t)(col0 + j) * a.K;
+            double sum = 0.0;
+            for (int k = lane; k < a.K; k += 32)
+                sum += (double)__bfloat162float(xr[k]) * (double)__bfloat162float(wr[k]);
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            if (lane == src) {
+                keep &= ~(1ull << j);
+                keep |= (uint64_t)(sum + (double)bias[j] > 0.0) << j;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ x7) << 4));
+        const uint4 e = *at;
+        uint32_t o[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int j = 8 * c + 2 * t;
+            o[t] &= ((keep >> j) & 1 ? 0xFFFFu : 0u) | ((keep >> (j + 1)) & 1 ? 0xFFFF0000u : 0u);
+            v[j] = o[t] << 16;
+            v[j + 1] = o[t] & 0xFFFF0000u;
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 }
 
 // Sums of 32 columns over the warp's 32 lanes: lane l returns column l's sum. Each step halves
@@ -444,7 +496,10 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                     __syncwarp();
                     tmem_ld_wait_regs(v);
-                    finish<MODE>(args.act, v, mybias + ci * 64, has_e, ob + lane * 128, lane & 7);
+                    if (MODE == LIN_GRAD && args.act == LIN_RELU)
+                        finish_row_relu_grad(v, mybias + ci * 64, ob + lane * 128, lane & 7, args, row0 + lane, col, lane);
+                    else
+                        finish<MODE>(args.act, v, mybias + ci * 64, has_e, ob + lane * 128, lane & 7);
                     if constexpr (MODE == LIN_GRAD) {
                         if (args.sums != nullptr) {
                             colsum[2 * ci] += column_sum32(v, lane);
