@@ -1159,13 +1159,13 @@ int map_attn(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t r
 }
 
 // bias [batch][n_windows][heads][32][128] as (slot, row, head, window, batch): boxes of one
-// window's 32 rows x 64 slots; windows past n_windows read as 0.
-int map_attn_bias(CUtensorMap *m, const void *t, const atomattn_params *p) {
+// window's 32 rows x 64 or 32 slots; windows past n_windows read as 0.
+int map_attn_bias(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t slots) {
     const uint64_t nw = (uint64_t)attn_windows(p), h = (uint64_t)p->heads;
     const uint64_t dims[5] = {128, 32, h, nw, (uint64_t)p->batch};
     const uint64_t strides[4] = {128 * 2, 32 * 128 * 2, h * 32 * 128 * 2, nw * h * 32 * 128 * 2};
-    const uint32_t box[5] = {64, 32, 1, 1, 1};
-    return encode(m, 5, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint32_t box[5] = {slots, 32, 1, 1, 1};
+    return encode(m, 5, t, dims, strides, box, slots == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // ---- linear layers ------------------------------------------------------------------
@@ -1606,7 +1606,7 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
         (rc = map_attn(&m.v, p->v, p, 256)))
         return rc;
     m.bias = m.q;  // unused without a bias
-    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p))) return rc;
+    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p, 64))) return rc;
     AttnArgs a;
     a.batch = p->batch;
     a.n = p->n_atoms;
@@ -1639,8 +1639,8 @@ int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn
         (rc = map_attn(&m.dout, dout, p, 32)))
         return rc;
     m.bias = m.dbias = m.q;  // unused without a bias
-    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p))) return rc;
-    if (g->dbias && (rc = map_attn_bias(&m.dbias, g->dbias, p))) return rc;
+    if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p, 32))) return rc;
+    if (g->dbias && (rc = map_attn_bias(&m.dbias, g->dbias, p, 32))) return rc;
     AttnBwdArgs a;
     memset(&a, 0, sizeof a);
     a.batch = p->batch;

@@ -7,48 +7,52 @@
 //
 // A key atom takes part in four consecutive windows. Keys are taken in groups of 32
 // (group g: atoms 32g - 48 .. 32g - 17); window w holds groups w .. w + 3. A block of
-// four warps walks down consecutive windows of one (batch, head): warp g mod 4 keeps
-// the fp32 sums dk and dv of group g in registers through the group's four windows and
-// then writes them once, so no sum leaves the chip unfinished, nothing is added
-// atomically, and q, k, v, dO and bias are each read once. A block owns a run of
-// groups; it first recomputes the three windows before its run, which the block
-// before owns, for their share of dk and dv.
+// four warps walks down consecutive windows of one (batch, head); group g belongs to warp
+// g mod 4 and stays with it through its four windows, so that q, k, v, dO and bias are
+// each read once. dk and dv of the four groups are sums in tensor memory, group g in lanes
+// 32 (g mod 4) ..: per window two tcgen05 products (128 keys x 32 channels x 32 queries,
+// P^T and dS^T as MN-major operands) add to all of them, and the warp whose group has seen
+// its last window reads its lanes, writes the 32 atoms' dk and dv, and clears them. No
+// partial sum leaves the chip and nothing is added atomically. A block owns a run of
+// groups; it first recomputes the three windows before its run, which the block before
+// owns, for their share of dk and dv.
 //
 // What bounds it: memory, 448 B per atom and head, and 512 B of bias and its gradient,
-// against 41 k operations. The five products run on the warp-level tensor instruction
-// (m16n8k16): at 32 x 128 x 32 per window a tcgen05 tile of 128 query rows would spend
-// seven eighths of each product outside the windows, and its accumulators would
-// have to leave tensor memory for the softmax and return through shared memory in two
-// layouts. The scores are held transposed, keys as rows: P^T and dS^T are then, as they
-// lie in registers, the left operands of dv and dk; only dS is turned, by a
-// transposing store into the bias's own tile, from which dq's product and the copy to
-// dbias both read.
+// against 41 k operations; and next to it the 4096 exponentials and gradients of each
+// window. Scores and dP run on the warp-level tensor instruction (m16n8k16): a warp
+// holds 32 queries x its 32 keys in registers, so a query's statistics take two shuffles
+// and one exchange of (maximum, sum of exponentials, sum of p dP) among the four warps.
+// (A tcgen05 tile of 128 query rows would spend most of S outside the windows, and bring
+// it back through tensor memory.) P goes to a tile of its own, dS to the bias's: both are
+// the tcgen05 products' left operands as they lie; dq (m16n8k16) and the copy to dbias read
+// dS there too. Keeping dk and dv in registers instead took 64 of them per lane: two blocks
+// an SM fitted then, four do now.
 //
-// Softmax across the four warps: each takes its own keys' maximum, sum of exponentials
-// and sum of p dP, and one exchange through shared memory joins the three.
-//
-// Copies: TMA, kStages windows in flight (64-byte rows with the 64-byte swizzle, bias
-// rows with the 128-byte one). Every wait is bounded.
+// Copies: TMA, kStages windows in flight (64-byte rows with the 64-byte swizzle; the bias as
+// four tiles of 32 slots, one per warp). Every wait is bounded.
 #include "kernels.h"
 
 namespace trimul {
 namespace ab {
 constexpr int QW = 32, KOFF = 48;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+constexpr int kBlocks = 4;                 // blocks per SM
 constexpr int RING = kStages + 3;          // key groups held: the window's four and those in flight
-constexpr int TILE = 32 * 64;              // 32 atoms of one head
-constexpr int BIAS_HALF = 32 * 128;        // 32 rows x 64 slots
-constexpr int BIAS = 2 * BIAS_HALF;
+constexpr int TILE = 32 * 64;              // 32 rows of 32 bf16
+constexpr int BIAS = 4 * TILE;             // [warp] 32 queries x the 32 slots of the warp's group
 constexpr int THREADS = 128;
-constexpr int OFF_BIAS = 0;                          // [kStages][2][32][64] bias, then dS
-constexpr int OFF_Q = OFF_BIAS + kStages * BIAS;     // [kStages] q
+constexpr int OFF_BIAS = 0;                          // [kStages] bias, then dS
+constexpr int OFF_P = OFF_BIAS + kStages * BIAS;     // P
+constexpr int OFF_Q = OFF_P + BIAS;                  // [kStages] q
 constexpr int OFF_DO = OFF_Q + kStages * TILE;       // [kStages] dO
 constexpr int OFF_K = OFF_DO + kStages * TILE;       // [RING] k
 constexpr int OFF_V = OFF_K + RING * TILE;           // [RING] v
-constexpr int OFF_RED = OFF_V + RING * TILE;         // [2][32][4] float4: each warp's max, sum, sum p dP
-constexpr int OFF_ROW = OFF_RED + 2 * 32 * 4 * 16;   // [4][32] float2: a warp's factor and delta per query
+constexpr int OFF_RED = OFF_V + RING * TILE;         // [4][32] float4: each warp's max, sum, sum p dP per query
+constexpr int OFF_ROW = OFF_RED + 4 * 32 * 16;       // [4][32] float2: a warp's factor and -delta per query
 constexpr int OFF_BAR = OFF_ROW + 4 * 32 * 8;
-constexpr size_t SMEM = 1024 + OFF_BAR + 64;
+constexpr size_t SMEM = 512 + OFF_BAR + 64;
+constexpr int DK_COL = 0, DV_COL = 32, TMEM_COLS = 64;
+static_assert(kBlocks * (SMEM + 1024) <= 233472, "shared memory of an SM");
 }  // namespace ab
 
 namespace {
@@ -65,10 +69,16 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// d += a b: 16 x 8 (fp32) from 16 x 16 and 16 x 8 (bf16).
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d = a b, d += a b: 16 x 8 (fp32) from 16 x 16 and 16 x 8 (bf16). d[0] holds row lane / 4, d[1] row
+// lane / 4 + 8, columns 2 (lane % 4) and the next.
+__device__ __forceinline__ void mma_first(float2 (&d)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0].x), "=f"(d[0].y), "=f"(d[1].x), "=f"(d[1].y)
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_next(float2 (&d)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float ex2_hw(float x) {
@@ -77,68 +87,109 @@ __device__ __forceinline__ float ex2_hw(float x) {
     return y;
 }
 
-// 16-byte chunk c (0..3) of row r in a tile of 64-byte rows (64-byte swizzle).
-__device__ __forceinline__ uint32_t at64(uint32_t tile, int r, int c) {
-    return tile + (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
-// 16-byte chunk c (0..15, 8 slots each) of row r in a bias tile (two halves of 128-byte rows).
-__device__ __forceinline__ uint32_t at128(uint32_t tile, int r, int c) {
-    return tile + (uint32_t)((c >> 3) * ab::BIAS_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+// Byte offset of 16-byte chunk c (0..3) of row r in a tile of 64-byte rows (64-byte swizzle). The
+// swizzle is an exclusive or, so a lane keeps the offset of its own row and chunk 0 or 1: chunk
+// c + 2 is that offset ^ 32, and 16 rows more add 1024.
+__device__ __forceinline__ uint32_t at64(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// Zeros in the warp's 32 lanes x 32 columns of tensor memory.
+__device__ __forceinline__ void tmem_zero32(uint32_t taddr) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(taddr),
+        "r"(0)
+        : "memory");
 }
 
-// A reduction over the eight lanes that share lane % 4, of eight values each: lane group
-// r = lane / 4 returns the result of value index r with its bits reversed (see value_of).
-template <typename Op>
-__device__ __forceinline__ float reduce_scatter8(const float (&x)[8], int lane, Op op) {
-    const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-    float y[4], z[2];
+// The sum, or the maximum, over the four lanes that hold one row of an accumulator.
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// s[32 queries][32 keys] = x[queries][32] y[keys][32]^T, tiles of 64-byte rows given as the lane's
+// addresses (rows as left and as right operand); s[16-row tile][8-key tile].
+__device__ __forceinline__ void product_32x32(float2 (&s)[2][4][2], uint32_t xa, uint32_t yb) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float keep = b4 ? x[i + 4] : x[i], give = b4 ? x[i] : x[i + 4];
-        y[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-    }
+    for (int kk = 0; kk < 2; ++kk) {
+        uint32_t a0[4], a1[4], b01[4], b23[4];
+        ldsm4(a0, xa ^ (32 * kk));
+        ldsm4(a1, (xa ^ (32 * kk)) + 1024);
+        ldsm4(b01, yb ^ (32 * kk));
+        ldsm4(b23, (yb ^ (32 * kk)) + 1024);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float keep = b3 ? y[i + 2] : y[i], give = b3 ? y[i] : y[i + 2];
-        z[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+        for (int mt = 0; mt < 2; ++mt) {
+            const uint32_t(&a)[4] = mt ? a1 : a0;
+            if (kk == 0) {
+                mma_first(s[mt][0], a, b01[0], b01[1]);
+                mma_first(s[mt][1], a, b01[2], b01[3]);
+                mma_first(s[mt][2], a, b23[0], b23[1]);
+                mma_first(s[mt][3], a, b23[2], b23[3]);
+            } else {
+                mma_next(s[mt][0], a, b01[0], b01[1]);
+                mma_next(s[mt][1], a, b01[2], b01[3]);
+                mma_next(s[mt][2], a, b23[0], b23[1]);
+                mma_next(s[mt][3], a, b23[2], b23[3]);
+            }
+        }
     }
-    const float keep = b2 ? z[1] : z[0], give = b2 ? z[0] : z[1];
-    return op(keep, __shfl_xor_sync(0xffffffffu, give, 4));
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(ab::THREADS, 3)
+__global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     atomattn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                         const __grid_constant__ CUtensorMap tmBias, const __grid_constant__ CUtensorMap tmDbias,
                         const AttnBwdArgs args) {
     using namespace ab;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *smem = smem_raw + ((512u - (smem_u32(smem_raw) & 511u)) & 511u);
     const uint32_t sbase = smem_u32(smem);
     float4 *red = reinterpret_cast<float4 *>(smem + OFF_RED);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);  // [kStages]
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(full + kStages);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + OFF_BAR);  // [kStages] window landed
+    uint64_t *summed = full + kStages;                               // the window's dk and dv products are done
+    uint64_t *drain = summed + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int quad = lane & 3, grp = lane >> 2;
     const KernelCtl &ctl = args.ctl;
     const int h = (int)(blockIdx.x % args.heads);
     const int rest = (int)(blockIdx.x / args.heads);
     const int chain = rest % args.chains, b = rest / args.chains;
     const int n = args.n, nw = args.n_windows;
-    // Groups (and windows' dq, dbias) this block owns: [s0, s1); its first window is s0 - 3.
+    // Groups (and windows' dq, dbias) this block owns: [s0, s1); it computes windows [first, wend).
     const int s0 = chain * args.per_chain, s1 = min(nw + 2, s0 + args.per_chain);
     const int first = max(0, s0 - 3), wend = min(nw, s1);
     const bool has_bias = args.has_bias != 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+        mbar_init(summed, 1);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     if (blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 
     // Loads of window s: its q, dO and bias into stage (s - first) % kStages, and the key group
@@ -154,301 +205,264 @@ __global__ void __launch_bounds__(ab::THREADS, 3)
             tma_load_3d(smem + OFF_K + slot * TILE, &tmK, &full[st], h * 32, g * 32 - KOFF, b);
             tma_load_3d(smem + OFF_V + slot * TILE, &tmV, &full[st], h * 32, g * 32 - KOFF, b);
         }
-        if (has_bias) {
-            tma_load_5d(smem + OFF_BIAS + st * BIAS, &tmBias, &full[st], 0, 0, h, s, b);
-            tma_load_5d(smem + OFF_BIAS + st * BIAS + BIAS_HALF, &tmBias, &full[st], 64, 0, h, s, b);
-        }
+        if (has_bias)
+            for (int x = 0; x < 4; ++x)
+                tma_load_5d(smem + OFF_BIAS + st * BIAS + x * TILE, &tmBias, &full[st], ((x - s) & 3) * 32, 0, h, s, b);
     };
     int issued = 0;  // thread 0: windows whose loads have been issued
     if (threadIdx.x == 0)
         for (; issued < kStages && first + issued < wend; ++issued) issue(first + issued);
 
-    float dk[2][4][4], dv[2][4][4];  // [16-key tile][8-channel tile] sums of this warp's group
-#pragma unroll
-    for (int i = 0; i < 32; ++i) (&dk[0][0][0])[i] = (&dv[0][0][0])[i] = 0.f;
     uint32_t vmask = 0;  // valid keys of this warp's group, bit = atom - first atom of the group
     const float scale = args.scale, log2e = 1.4426950408889634f;
     const size_t row_elems = (size_t)args.heads * 32;
-    // ldmatrix / stmatrix lane coordinates: row and chunk of the matrix a lane addresses.
-    const int la_r = (lane & 7) + ((lane >> 3) & 1) * 8, la_c = lane >> 4;  // 16 rows, 2 chunks
-    const int lb_r = (lane & 7) + (lane >> 4) * 8, lb_c = (lane >> 3) & 1;
+    // ldmatrix / stmatrix lane addresses within a tile: rows as a left operand's, as a right operand's.
+    const uint32_t a64 = at64((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t b64 = at64((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const int q0 = (warp & 1) * 16, c0 = (warp >> 1) * 2;  // dq: this warp's 16 queries, and 16 channels from 8 c0
+    const uint32_t mytmem = tmem + ((uint32_t)(warp * 32) << 16);
+    auto ring_at = [&](int base, int j) { return base + j < RING ? base + j : base + j - RING; };
+
+    // dk and dv of group g, whose windows are all summed, from this warp's lanes: lane = atom.
+    auto write_group = [&](int g) {
+        if (g < s0 || g >= s1) return;  // warp-uniform: another block's
+        const int atom = g * 32 - KOFF + lane;
+        const bool valid = (vmask >> lane) & 1u;
+        __nv_bfloat16 *out[2] = {args.dk, args.dv};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            uint32_t v[32];
+            tmem_ld32(mytmem + (x ? DV_COL : DK_COL), v);
+            tmem_ld_wait_regs(v);
+            if (atom >= 0 && atom < n) {
+                uint4 *dst = reinterpret_cast<uint4 *>(out[x] + ((size_t)b * n + atom) * row_elems + h * 32);
+                const float f = x ? 1.f : scale;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        o[t] = valid ? pack_bf16x2(__uint_as_float(v[8 * c + 2 * t]) * f, __uint_as_float(v[8 * c + 2 * t + 1]) * f)
+                                     : 0u;
+                    dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    };
 
     bool ok = true;
-    int seen = -1;  // the group whose keys this warp has looked at
-    for (int s = first; s < s1; ++s) {
-        const int i = s - first;
-        const int pos = (warp - s) & 3, g = s + pos;  // this warp's group and its place in the window
-        if (s < wend) {
-            const int st = i % kStages, slot = (g - first) % RING;
-            const uint32_t kt = sbase + OFF_K + slot * TILE, vt = sbase + OFF_V + slot * TILE;
-            const uint32_t qt = sbase + OFF_Q + st * TILE, dot_ = sbase + OFF_DO + st * TILE;
-            const uint32_t bt = sbase + OFF_BIAS + st * BIAS;
-            float sc[2][4][4], dp[2][4][4];  // [16-key tile][8-query tile]: scores, then P; dP, then dS
-            ok = warp_wait(&full[st], (uint32_t)(i / kStages) & 1u, abort_flag, ctl, SITE_ATB | 1, s);
-            if (ok) {
-                if (g != seen) {
-                    // New keys: which are valid. Masked ones are zeroed, so that what is stored there
-                    // (anything, infinities and NaN included) meets a zero weight as a zero.
-                    const int atom = g * 32 - KOFF + lane;
-                    bool valid = atom >= 0 && atom < n;
-                    if (valid && args.mask) valid = (__ldg(reinterpret_cast<const uint16_t *>(args.mask) + (size_t)b * n + atom) & 0x7FFFu) != 0;
-                    vmask = __ballot_sync(0xffffffffu, valid);
-                    if (!valid) {
+    int st = 0, base = 0;  // stage of window s, ring slot of group s
+    uint32_t phase = 0;
+    for (int s = first; s < wend; ++s) {
+        const int i = s - first, pos = (warp - s) & 3;  // the place of this warp's group in the window
+        const int slot = ring_at(base, pos);
+        const uint32_t qa = sbase + OFF_Q + st * TILE + a64, oa = sbase + OFF_DO + st * TILE + a64;
+        const uint32_t bt = sbase + OFF_BIAS + st * BIAS, mine = bt + warp * TILE + a64, pt = sbase + OFF_P + warp * TILE + a64;
+        // [16-query tile][8-key tile][row, row + 8]: scores, then p; dP, then dS.
+        float2 sc[2][4][2], dp[2][4][2];
+        // The sums of the window before: its operands' tiles are free, and its oldest group is complete.
+        ok = i == 0 || warp_wait(summed, (uint32_t)(i - 1) & 1u, abort_flag, ctl, SITE_ATB | 2, s);
+        ok = ok && warp_wait(&full[st], phase, abort_flag, ctl, SITE_ATB | 1, s);
+        if (ok) {
+            if (pos == 3 || i == 0) {  // a new group
+                if (i > 0) {
+                    tc_fence_after();
+                    write_group(s - 1);
+                }
+                tmem_zero32(mytmem + DK_COL);
+                tmem_zero32(mytmem + DV_COL);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                // Which of its keys are valid. Masked ones are zeroed, so that what is stored there (anything,
+                // infinities and NaN included) meets a zero weight as a zero.
+                const int atom = (s + pos) * 32 - KOFF + lane;
+                bool valid = atom >= 0 && atom < n;
+                if (valid && args.mask) valid = (__ldg(reinterpret_cast<const uint16_t *>(args.mask) + (size_t)b * n + atom) & 0x7FFFu) != 0;
+                vmask = __ballot_sync(0xffffffffu, valid);
+                if (!valid) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            *reinterpret_cast<uint4 *>(smem + OFF_K + slot * TILE + lane * 64 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(smem + OFF_V + slot * TILE + lane * 64 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();  // the slot is TMA's again later
+                    for (int c = 0; c < 4; ++c) {
+                        *reinterpret_cast<uint4 *>(smem + OFF_K + slot * TILE + lane * 64 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(smem + OFF_V + slot * TILE + lane * 64 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    __syncwarp();
-                    seen = g;
+                    fence_proxy_async_smem();  // the slot is TMA's again later
                 }
-                // Scores and dP, transposed: 32 keys x 32 queries.
+                __syncwarp();
+            }
+            product_32x32(sc, qa, sbase + OFF_K + slot * TILE + b64);
+            product_32x32(dp, oa, sbase + OFF_V + slot * TILE + b64);
+            // Logits; -inf where the key is not valid or the query is past the sequence.
+            const float2 sc2 = make_float2(scale, scale);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) (&sc[0][0][0])[x] = (&dp[0][0][0])[x] = 0.f;
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t a0[4], a1[4], b01[4], b23[4];
-                    ldsm4(a0, at64(kt, la_r, kk * 2 + la_c));
-                    ldsm4(a1, at64(kt, 16 + la_r, kk * 2 + la_c));
-                    ldsm4(b01, at64(qt, lb_r, kk * 2 + lb_c));
-                    ldsm4(b23, at64(qt, 16 + lb_r, kk * 2 + lb_c));
-                    mma16816(sc[0][0], a0, b01[0], b01[1]);
-                    mma16816(sc[0][1], a0, b01[2], b01[3]);
-                    mma16816(sc[0][2], a0, b23[0], b23[1]);
-                    mma16816(sc[0][3], a0, b23[2], b23[3]);
-                    mma16816(sc[1][0], a1, b01[0], b01[1]);
-                    mma16816(sc[1][1], a1, b01[2], b01[3]);
-                    mma16816(sc[1][2], a1, b23[0], b23[1]);
-                    mma16816(sc[1][3], a1, b23[2], b23[3]);
+                for (int np = 0; np < 2; ++np) {
+                    uint32_t bw[4] = {0u, 0u, 0u, 0u};  // (row, row + 8) of key tile 2 np, then of 2 np + 1
+                    if (has_bias) ldsm4(bw, (mine ^ (32 * np)) + 1024 * mt);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float2 &l = sc[mt][2 * np + (x >> 1)][x & 1];
+                        l = __ffma2_rn(l, sc2, make_float2(__uint_as_float(bw[x] << 16), __uint_as_float(bw[x] & 0xFFFF0000u)));
+                    }
                 }
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    uint32_t a0[4], a1[4], b01[4], b23[4];
-                    ldsm4(a0, at64(vt, la_r, kk * 2 + la_c));
-                    ldsm4(a1, at64(vt, 16 + la_r, kk * 2 + la_c));
-                    ldsm4(b01, at64(dot_, lb_r, kk * 2 + lb_c));
-                    ldsm4(b23, at64(dot_, 16 + lb_r, kk * 2 + lb_c));
-                    mma16816(dp[0][0], a0, b01[0], b01[1]);
-                    mma16816(dp[0][1], a0, b01[2], b01[3]);
-                    mma16816(dp[0][2], a0, b23[0], b23[1]);
-                    mma16816(dp[0][3], a0, b23[2], b23[3]);
-                    mma16816(dp[1][0], a1, b01[0], b01[1]);
-                    mma16816(dp[1][1], a1, b01[2], b01[3]);
-                    mma16816(dp[1][2], a1, b23[0], b23[1]);
-                    mma16816(dp[1][3], a1, b23[2], b23[3]);
-                }
-                // Logits; -inf where the key is not valid or the query is past the sequence.
+            if (vmask != 0xFFFFFFFFu) {
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
-                    uint32_t bw[4] = {0u, 0u, 0u, 0u};  // key blocks of 8: (16-key tile 0, 0), (0, +8), (1, 0), (1, +8)
-                    if (has_bias) ldsm4_t(bw, at128(bt, nt * 8 + (lane & 7), pos * 4 + (lane >> 3)));
+                    const uint32_t two = vmask >> (8 * nt + 2 * quad);
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t w = bw[2 * mt + r];
-                            sc[mt][nt][2 * r] = fmaf(sc[mt][nt][2 * r], scale, __uint_as_float(w << 16));
-                            sc[mt][nt][2 * r + 1] = fmaf(sc[mt][nt][2 * r + 1], scale, __uint_as_float(w & 0xFFFF0000u));
-                        }
+                    for (int x = 0; x < 4; ++x) {
+                        float2 &l = sc[x >> 1][nt][x & 1];
+                        if (!(two & 1u)) l.x = -INFINITY;
+                        if (!(two & 2u)) l.y = -INFINITY;
+                    }
                 }
-                if (vmask != 0xFFFFFFFFu) {
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r)
-                            if (!((vmask >> (16 * mt + 8 * r + grp)) & 1u))
-#pragma unroll
-                                for (int nt = 0; nt < 4; ++nt) sc[mt][nt][2 * r] = sc[mt][nt][2 * r + 1] = -INFINITY;
-                }
-                const int left = n - s * QW;  // queries of this window
-                if (left < QW) {
-#pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (nt * 8 + 2 * quad + e >= left)
-#pragma unroll
-                                for (int mt = 0; mt < 2; ++mt) sc[mt][nt][e] = sc[mt][nt][2 + e] = -INFINITY;
-                }
-                // This warp's maximum per query (column nt * 8 + 2 quad + e; index 2 nt + e), to all lanes.
-                float mx[8], sum[8], dot[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int nt = c >> 1, e = c & 1;
-                    mx[c] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
-                    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
-                    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
-                    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
-                }
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int nt = c >> 1, e = c & 1;
-                    const float m = mx[c] == -INFINITY ? 0.f : mx[c];
-                    sum[c] = 0.f;
-                    dot[c] = 0.f;
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            // The difference before the factor: logits next to the type's lowest value stay finite.
-                            const float p = ex2_hw((sc[mt][nt][2 * r + e] - m) * log2e);
-                            sc[mt][nt][2 * r + e] = p;
-                            sum[c] += p;
-                            dot[c] = fmaf(p, dp[mt][nt][2 * r + e], dot[c]);
-                        }
-                }
-                const auto add = [](float x, float y) { return x + y; };
-                const float tsum = reduce_scatter8(sum, lane, add), tdot = reduce_scatter8(dot, lane, add);
-                // Lane group grp holds column index c with bits (16, 8, 4) of the lane as its bits (4, 2, 1).
-                const int c = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-                float tmax = mx[0];
-#pragma unroll
-                for (int x = 1; x < 8; ++x) tmax = c == x ? mx[x] : tmax;
-                const int col = (c >> 1) * 8 + 2 * quad + (c & 1);
-                red[((i & 1) * 32 + col) * 4 + warp] = make_float4(tmax, tsum, tdot, 0.f);
             }
-            // Every warp's part is there; and every warp is done with the window before.
-            ok = __syncthreads_and(ok);
-            if (!ok) break;
-            if (threadIdx.x == 0 && i > 0 && first + issued < wend) {
-                // The stage of window s - 1 and the ring slot of group s - 1 are free once the copy of its dbias
-                // has read the tile.
-                tma_store_wait_read<0>();
-                issue(first + issued);
-                ++issued;
+            const int left = n - s * QW;  // queries of this window
+            if (left < QW) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (8 * x + grp >= left)
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt) sc[x >> 1][nt][x & 1] = make_float2(-INFINITY, -INFINITY);
             }
-            float2 *rowv = reinterpret_cast<float2 *>(smem + OFF_ROW) + warp * 32;
-            {
-                const float4 *r4 = red + ((i & 1) * 32 + lane) * 4;
-                float4 v[4];
+            // Over this warp's keys, for each of the lane's four queries (8 x + grp): the maximum, the
+            // sum of p = exp(l - maximum) and the sum of p dP.
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = r4[x];
-                const float m = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-                float total = 0.f, dots = 0.f, mine = 0.f;
+            for (int x = 0; x < 4; ++x) {
+                const int mt = x >> 1, r = x & 1;
+                float mx = fmaxf(sc[mt][0][r].x, sc[mt][0][r].y);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float f = v[x].x == -INFINITY ? 0.f : ex2_hw((v[x].x - m) * log2e);
-                    total = fmaf(f, v[x].y, total);
-                    dots = fmaf(f, v[x].z, dots);
-                    if (x == warp) mine = f;
+                for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(sc[mt][nt][r].x, sc[mt][nt][r].y));
+                mx = quad_max(mx);
+                const float m = mx == -INFINITY ? 0.f : mx;
+                const float2 nm = make_float2(-m, -m), l2 = make_float2(log2e, log2e);
+                float2 sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    // The difference before the factor: logits next to the type's lowest value stay finite.
+                    const float2 t = __fmul2_rn(__fadd2_rn(sc[mt][nt][r], nm), l2);
+                    const float2 p = make_float2(ex2_hw(t.x), ex2_hw(t.y));
+                    sc[mt][nt][r] = p;
+                    sum = __fadd2_rn(sum, p);
+                    dot = __ffma2_rn(p, dp[mt][nt][r], dot);
                 }
-                const float inv = total == 0.f ? 0.f : 1.f / total;  // a query without a valid key: P = 0
-                rowv[lane] = make_float2(mine * inv, dots * inv);
+                const float tsum = quad_sum(sum.x + sum.y), tdot = quad_sum(dot.x + dot.y);
+                if (quad == x) red[warp * 32 + 8 * x + grp] = make_float4(mx, tsum, tdot, 0.f);
+            }
+        }
+        // Every warp's part is there; and every warp is done with the window before.
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        if (threadIdx.x == 0 && i > 0 && first + issued < wend) {
+            // The stage of window s - 1 and the ring slot of group s - 1 are free once the copy of its dbias
+            // has read the tile.
+            tma_store_wait_read<0>();
+            issue(first + issued);
+            ++issued;
+        }
+        float2 *rowv = reinterpret_cast<float2 *>(smem + OFF_ROW) + warp * 32;
+        {
+            float4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = red[32 * x + lane];
+            const float m = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+            float total = 0.f, dots = 0.f, own = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float f = v[x].x == -INFINITY ? 0.f : ex2_hw((v[x].x - m) * log2e);
+                total = fmaf(f, v[x].y, total);
+                dots = fmaf(f, v[x].z, dots);
+                if (x == warp) own = f;
+            }
+            const float inv = total == 0.f ? 0.f : 1.f / total;  // a query without a valid key: P = 0
+            rowv[lane] = make_float2(own * inv, -dots * inv);
+        }
+        __syncwarp();
+        // P and dS, each rounded once to bf16, the type of the products' other operands.
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t pb[4][2], ds[4][2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float2 fd = rowv[16 * mt + 8 * r + grp];
+                const float2 f2 = make_float2(fd.x, fd.x), nd = make_float2(fd.y, fd.y);
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const float2 p = __fmul2_rn(sc[mt][nt][r], f2);
+                    const float2 d = __fmul2_rn(p, __fadd2_rn(dp[mt][nt][r], nd));
+                    pb[nt][r] = pack_bf16x2(p.x, p.y);
+                    ds[nt][r] = pack_bf16x2(d.x, d.y);
+                }
+            }
+            stsm4(pt + 1024 * mt, pb[0][0], pb[0][1], pb[1][0], pb[1][1]);
+            stsm4((pt ^ 32) + 1024 * mt, pb[2][0], pb[2][1], pb[3][0], pb[3][1]);
+            stsm4(mine + 1024 * mt, ds[0][0], ds[0][1], ds[1][0], ds[1][1]);
+            stsm4((mine ^ 32) + 1024 * mt, ds[2][0], ds[2][1], ds[3][0], ds[3][1]);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();  // P and dS of all 128 slots are in their tiles
+        if (threadIdx.x == 32) {
+            // dv += P^T dO, dk += dS^T q: 128 keys (group g mod 4 in lanes 32 (g mod 4) ..) x 32 channels,
+            // K = 32 queries in two steps; tiles of 32 keys are 2 KB apart.
+            tc_fence_after();
+            const uint32_t idesc = idesc_bf16(128, 32, 1, 1);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const uint32_t q_at = sbase + OFF_Q + st * TILE + 1024 * kk, o_at = sbase + OFF_DO + st * TILE + 1024 * kk;
+                mma_bf16(tmem + DV_COL, sdesc_sw64(sbase + OFF_P + 1024 * kk, TILE, 512), sdesc_sw64(o_at, TILE, 512), idesc, 1u);
+                mma_bf16(tmem + DK_COL, sdesc_sw64(bt + 1024 * kk, TILE, 512), sdesc_sw64(q_at, TILE, 512), idesc, 1u);
+            }
+            mma_commit(summed);
+        }
+        if (s >= s0) {
+            if (args.has_dbias && threadIdx.x == 0) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    tma_store_5d(&tmDbias, smem + OFF_BIAS + st * BIAS + x * TILE, ((x - s) & 3) * 32, 0, h, s, b);
+                tma_store_commit();
             }
             __syncwarp();
-            // P and dS.
+            float2 dq[2][2];
+            const uint32_t da = bt + a64 + q0 * 64, ka = sbase + OFF_K + (a64 ^ (c0 << 4));
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const float4 fd = *reinterpret_cast<const float4 *>(&rowv[nt * 8 + 2 * quad]);
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float p0 = sc[mt][nt][2 * r] * fd.x, p1 = sc[mt][nt][2 * r + 1] * fd.z;
-                        sc[mt][nt][2 * r] = p0;
-                        sc[mt][nt][2 * r + 1] = p1;
-                        dp[mt][nt][2 * r] = p0 * (dp[mt][nt][2 * r] - fd.y);
-                        dp[mt][nt][2 * r + 1] = p1 * (dp[mt][nt][2 * r + 1] - fd.w);
-                    }
-            }
-            // bf16 operands: P and dS are rounded once, to the type of the products' other operands.
-            uint32_t ds[2][4][2];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) ds[mt][nt][r] = pack_bf16x2(dp[mt][nt][2 * r], dp[mt][nt][2 * r + 1]);
-                stmatrix_x4_trans(at128(bt, nt * 8 + (lane & 7), pos * 4 + (lane >> 3)), ds[0][nt][0], ds[0][nt][1],
-                                  ds[1][nt][0], ds[1][nt][1]);
-            }
-            fence_proxy_async_smem();
-            if (g >= s0 && g < s1) {
-#pragma unroll
-                for (int kq = 0; kq < 2; ++kq) {
-                    uint32_t pa[2][4], sa[2][4];
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        pa[mt][0] = pack_bf16x2(sc[mt][2 * kq][0], sc[mt][2 * kq][1]);
-                        pa[mt][1] = pack_bf16x2(sc[mt][2 * kq][2], sc[mt][2 * kq][3]);
-                        pa[mt][2] = pack_bf16x2(sc[mt][2 * kq + 1][0], sc[mt][2 * kq + 1][1]);
-                        pa[mt][3] = pack_bf16x2(sc[mt][2 * kq + 1][2], sc[mt][2 * kq + 1][3]);
-                        sa[mt][0] = ds[mt][2 * kq][0];
-                        sa[mt][1] = ds[mt][2 * kq][1];
-                        sa[mt][2] = ds[mt][2 * kq + 1][0];
-                        sa[mt][3] = ds[mt][2 * kq + 1][1];
-                    }
-#pragma unroll
-                    for (int nd = 0; nd < 2; ++nd) {
-                        uint32_t bo[4], bq[4];
-                        ldsm4_t(bo, at64(dot_, kq * 16 + la_r, nd * 2 + la_c));
-                        ldsm4_t(bq, at64(qt, kq * 16 + la_r, nd * 2 + la_c));
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) {
-                            mma16816(dv[mt][2 * nd], pa[mt], bo[0], bo[1]);
-                            mma16816(dv[mt][2 * nd + 1], pa[mt], bo[2], bo[3]);
-                            mma16816(dk[mt][2 * nd], sa[mt], bq[0], bq[1]);
-                            mma16816(dk[mt][2 * nd + 1], sa[mt], bq[2], bq[3]);
-                        }
-                    }
+            for (int kk = 0; kk < 8; ++kk) {  // tile x = kk / 2 holds the group of warp x
+                uint32_t a[4], bk[4];
+                ldsm4(a, (da ^ (32 * (kk & 1))) + (kk >> 1) * TILE);
+                ldsm4_t(bk, ka + ring_at(base, ((kk >> 1) - s) & 3) * TILE + (kk & 1) * 1024);
+                if (kk == 0) {
+                    mma_first(dq[0], a, bk[0], bk[1]);
+                    mma_first(dq[1], a, bk[2], bk[3]);
+                } else {
+                    mma_next(dq[0], a, bk[0], bk[1]);
+                    mma_next(dq[1], a, bk[2], bk[3]);
                 }
             }
-            __syncthreads();  // dS of all 128 slots is in the tile
-            if (s >= s0) {
-                if (args.has_dbias && threadIdx.x == 0) {
-                    tma_store_5d(&tmDbias, smem + OFF_BIAS + st * BIAS, 0, 0, h, s, b);
-                    tma_store_5d(&tmDbias, smem + OFF_BIAS + st * BIAS + BIAS_HALF, 64, 0, h, s, b);
-                    tma_store_commit();
-                }
-                // dq: warp (x, y) takes queries 16 x .. and channels 16 y ..
-                const int q0 = (warp & 1) * 16, c0 = (warp >> 1) * 2;
-                float dq[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    uint32_t a[4], bk[4];
-                    const uint32_t kg = sbase + OFF_K + ((s + (kk >> 1) - first) % RING) * TILE;
-                    ldsm4(a, at128(bt, q0 + la_r, kk * 2 + la_c));
-                    ldsm4_t(bk, at64(kg, (kk & 1) * 16 + la_r, c0 + la_c));
-                    mma16816(dq[0], a, bk[0], bk[1]);
-                    mma16816(dq[1], a, bk[2], bk[3]);
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int atom = s * QW + q0 + 8 * r + grp;
-                    if (atom < n) {
-                        __nv_bfloat16 *dst = args.dq + ((size_t)b * n + atom) * row_elems + h * 32 + c0 * 8 + 2 * quad;
-                        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(dq[0][2 * r] * scale, dq[0][2 * r + 1] * scale);
-                        *reinterpret_cast<uint32_t *>(dst + 8) = pack_bf16x2(dq[1][2 * r] * scale, dq[1][2 * r + 1] * scale);
-                    }
+            for (int r = 0; r < 2; ++r) {
+                const int atom = s * QW + q0 + 8 * r + grp;
+                if (atom < n) {
+                    __nv_bfloat16 *dst = args.dq + ((size_t)b * n + atom) * row_elems + h * 32 + c0 * 8 + 2 * quad;
+                    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(dq[0][r].x * scale, dq[0][r].y * scale);
+                    *reinterpret_cast<uint32_t *>(dst + 8) = pack_bf16x2(dq[1][r].x * scale, dq[1][r].y * scale);
                 }
             }
         }
-        // Group s has seen its last window.
-        if (pos == 0) {
-            if (s >= s0) {
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int at = 16 * mt + 8 * r + grp, atom = g * 32 - KOFF + at;
-                        if (atom >= 0 && atom < n) {
-                            const bool valid = (vmask >> at) & 1u;
-                            const size_t off = ((size_t)b * n + atom) * row_elems + h * 32 + 2 * quad;
-#pragma unroll
-                            for (int nt = 0; nt < 4; ++nt) {
-                                *reinterpret_cast<uint32_t *>(args.dk + off + 8 * nt) =
-                                    valid ? pack_bf16x2(dk[mt][nt][2 * r] * scale, dk[mt][nt][2 * r + 1] * scale) : 0u;
-                                *reinterpret_cast<uint32_t *>(args.dv + off + 8 * nt) =
-                                    valid ? pack_bf16x2(dv[mt][nt][2 * r], dv[mt][nt][2 * r + 1]) : 0u;
-                            }
-                        }
-                    }
-            }
-#pragma unroll
-            for (int x = 0; x < 32; ++x) (&dk[0][0][0])[x] = (&dv[0][0][0])[x] = 0.f;
+        if (++st == kStages) {
+            st = 0;
+            phase ^= 1u;
         }
+        base = ring_at(base, 1);
+    }
+    // The groups of the last window: those this block owns have no window after it.
+    if (ok) {
+        const int last = wend - 1;
+        if (warp_wait(summed, (uint32_t)(last - first) & 1u, abort_flag, ctl, SITE_ATB | 3, last)) {
+            tc_fence_after();
+            write_group(last + ((warp - last) & 3));
+        }
+    } else if (threadIdx.x == 32) {
+        mma_commit(drain);  // no product may still be running when the block leaves
+        wait_drain(drain, 0, ctl.timeout_ns);
     }
     if (threadIdx.x == 0) {
         // No copy may be in flight when the block leaves (loads: only after a timeout).
@@ -456,6 +470,10 @@ __global__ void __launch_bounds__(ab::THREADS, 3)
             wait_drain(&full[x % kStages], (uint32_t)(x / kStages) & 1u, ctl.timeout_ns);
         tma_store_wait_all<0>();
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
 
 size_t atomattn_bwd_smem() { return ab::SMEM; }
@@ -465,9 +483,9 @@ cudaError_t atomattn_bwd_setup() {
 }
 
 cudaError_t launch_atomattn_bwd(const AttnBwdMaps &m, AttnBwdArgs a, int sms, cudaStream_t s) {
-    // The shortest runs that still fit one wave of three blocks an SM: a block's work is its run and
+    // The shortest runs that still fit one wave of kBlocks blocks an SM: a block's work is its run and
     // three windows more, so long sequences get long runs and short ones little depth.
-    const long long pairs = (long long)a.batch * a.heads, wave = 3ll * sms;
+    const long long pairs = (long long)a.batch * a.heads, wave = (long long)ab::kBlocks * sms;
     const int steps = a.n_windows + 2;
     long long chains = wave / pairs;
     if (chains < 1) chains = 1;

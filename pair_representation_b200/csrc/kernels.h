@@ -280,7 +280,7 @@ struct AttnBwdArgs {
 
 struct AttnBwdMaps {
     CUtensorMap q, k, v, dout;  // 3-D (heads * 32, n, batch), boxes (32, 32, 1), swizzle 64B
-    CUtensorMap bias, dbias;    // as AttnMaps::bias
+    CUtensorMap bias, dbias;    // 5-D as AttnMaps::bias, boxes (32, 32, 1, 1, 1), swizzle 64B
 };
 
 cudaError_t atomattn_bwd_setup();
