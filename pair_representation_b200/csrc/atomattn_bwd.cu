@@ -223,32 +223,46 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     const uint32_t mytmem = tmem + ((uint32_t)(warp * 32) << 16);
     auto ring_at = [&](int base, int j) { return base + j < RING ? base + j : base + j - RING; };
 
-    // dk and dv of group g, whose windows are all summed, from this warp's lanes: lane = atom.
-    auto write_group = [&](int g) {
-        if (g < s0 || g >= s1) return;  // warp-uniform: another block's
-        const int atom = g * 32 - KOFF + lane;
-        const bool valid = (vmask >> lane) & 1u;
-        __nv_bfloat16 *out[2] = {args.dk, args.dv};
+    // dk and dv of group g, whose windows are all summed, from this warp's lanes (lane = atom); with
+    // `clear` the lanes are set to 0 for the warp's next group.
+    auto write_group = [&](int g, bool clear) {
+        if (g >= s0 && g < s1) {  // warp-uniform; else another block's
+            const int atom = g * 32 - KOFF + lane;
+            const bool inside = atom >= 0 && atom < n, valid = (vmask >> lane) & 1u;
+            const size_t off = ((size_t)b * n + atom) * row_elems + h * 32;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            uint32_t v[32];
-            tmem_ld32(mytmem + (x ? DV_COL : DK_COL), v);
-            tmem_ld_wait_regs(v);
-            if (atom >= 0 && atom < n) {
-                uint4 *dst = reinterpret_cast<uint4 *>(out[x] + ((size_t)b * n + atom) * row_elems + h * 32);
-                const float f = x ? 1.f : scale;
+            for (int x = 0; x < 2; ++x) {
+                uint32_t v[32];
+                tmem_ld32(mytmem + (x ? DV_COL : DK_COL), v);
+                tmem_ld_wait_regs(v);
+                if (clear) tmem_zero32(mytmem + (x ? DV_COL : DK_COL));
+                if (inside) {
+                    uint4 *dst = reinterpret_cast<uint4 *>((x ? args.dv : args.dk) + off);
+                    const float f = x ? 1.f : scale;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[4];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        o[t] = valid ? pack_bf16x2(__uint_as_float(v[8 * c + 2 * t]) * f, __uint_as_float(v[8 * c + 2 * t + 1]) * f)
-                                     : 0u;
-                    dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int t = 0; t < 4; ++t)
+                            o[t] = valid ? pack_bf16x2(__uint_as_float(v[8 * c + 2 * t]) * f,
+                                                       __uint_as_float(v[8 * c + 2 * t + 1]) * f)
+                                         : 0u;
+                        dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
                 }
             }
+        } else if (clear) {
+            tmem_zero32(mytmem + DK_COL);
+            tmem_zero32(mytmem + DV_COL);
         }
     };
+    // Whether this lane's key of group g is valid, as the mask's bits (0: not). Asked a window ahead.
+    auto key_bits = [&](int g) -> uint16_t {
+        const int atom = g * 32 - KOFF + lane;
+        if (atom < 0 || atom >= n) return 0;
+        return args.mask ? __ldg(reinterpret_cast<const uint16_t *>(args.mask) + (size_t)b * n + atom) : (uint16_t)0x3F80u;
+    };
+    uint16_t key = key_bits(first + ((warp - first) & 3));
 
     bool ok = true;
     int st = 0, base = 0;  // stage of window s, ring slot of group s
@@ -267,17 +281,14 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
             if (pos == 3 || i == 0) {  // a new group
                 if (i > 0) {
                     tc_fence_after();
-                    write_group(s - 1);
+                    write_group(s - 1, true);
+                } else {
+                    tmem_zero32(mytmem + DK_COL);
+                    tmem_zero32(mytmem + DV_COL);
                 }
-                tmem_zero32(mytmem + DK_COL);
-                tmem_zero32(mytmem + DV_COL);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
                 // Which of its keys are valid. Masked ones are zeroed, so that what is stored there (anything,
                 // infinities and NaN included) meets a zero weight as a zero.
-                const int atom = (s + pos) * 32 - KOFF + lane;
-                bool valid = atom >= 0 && atom < n;
-                if (valid && args.mask) valid = (__ldg(reinterpret_cast<const uint16_t *>(args.mask) + (size_t)b * n + atom) & 0x7FFFu) != 0;
+                const bool valid = (key & 0x7FFFu) != 0;
                 vmask = __ballot_sync(0xffffffffu, valid);
                 if (!valid) {
 #pragma unroll
@@ -288,6 +299,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                     fence_proxy_async_smem();  // the slot is TMA's again later
                 }
                 __syncwarp();
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
             }
             product_32x32(sc, qa, sbase + OFF_K + slot * TILE + b64);
             product_32x32(dp, oa, sbase + OFF_V + slot * TILE + b64);
@@ -360,6 +373,7 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
             issue(first + issued);
             ++issued;
         }
+        if (pos == 0) key = key_bits(s + 4);  // the warp's next group
         float2 *rowv = reinterpret_cast<float2 *>(smem + OFF_ROW) + warp * 32;
         {
             float4 v[4];
@@ -458,7 +472,7 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         const int last = wend - 1;
         if (warp_wait(summed, (uint32_t)(last - first) & 1u, abort_flag, ctl, SITE_ATB | 3, last)) {
             tc_fence_after();
-            write_group(last + ((warp - last) & 3));
+            write_group(last + ((warp - last) & 3), false);
         }
     } else if (threadIdx.x == 32) {
         mma_commit(drain);  // no product may still be running when the block leaves
