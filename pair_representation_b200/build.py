@@ -20,7 +20,7 @@ LIB = os.path.join(LIB_DIR, "libtrimul_b200.so")
 SOURCES = ["api.cu", "prologue_tc.cu", "contract_tc.cu", "epilogue_tc.cu", "simt_f32.cu", "noalloc.cu",
            "backward.cu", "atomattn_tc.cu", "mx_tc.cu", "atomattn_bwd.cu", "linear_tc.cu",
            "act8.cu"]
-HEADERS = ["common.cuh", "kernels.h", "tile_ops.cuh", "mx_block.cuh"]
+HEADERS = ["common.cuh", "kernels.h", "tile_ops.cuh", "mx_block.cuh", "linear_act.cuh"]
 
 
 def nvcc() -> str:

@@ -24,6 +24,7 @@
 //
 // Every wait is bounded; on a timeout the CTA lets its copies land and returns.
 #include "kernels.h"
+#include "linear_act.cuh"
 
 namespace trimul {
 namespace lin {
@@ -81,84 +82,41 @@ struct Tiles {
 
 namespace {
 
-__device__ __forceinline__ float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcpf(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
-// exp(-p) and 1 / (1 + exp(-p)) by the hardware's ex2 and rcp (relative errors about 2^-22), far
-// under the half step 2^-9 of the bf16 result. NaN stays NaN.
-__device__ __forceinline__ float exp_neg(float p) { return ex2f(p * -1.4426950408889634f); }
-
-template <int ACT>
-__device__ __forceinline__ float act_fwd(float p) {
-    if (ACT == LIN_RELU) return max_nan(p, 0.f);
-    if (ACT == LIN_NONE) return p;
-    const float s = rcpf(1.f + exp_neg(p));  // 0 where exp(-p) is infinite
-    return ACT == LIN_SIGMOID ? s : p * s;
-}
-
-// 1 - s is taken as s exp(-p), which keeps its digits where s is next to 1. p stops at -87, where
-// both factors are still finite and every slope is under 2e-36.
-template <int ACT>
-__device__ __forceinline__ float act_grad(float p, float d) {
-    if (ACT == LIN_NONE) return d;
-    p = max_nan(p, -87.f);
-    const float e = exp_neg(p), s = rcpf(1.f + e), c = s * e;
-    return ACT == LIN_SIGMOID ? d * (s * c) : d * fmaf(p * s, c, s);
-}
-
-// The 64 columns of one accumulator row: + bias, activation, residual (or the gradient), packed
-// to bf16 into the row's 128 swizzled bytes. In LIN_GRAD v receives the unrounded values.
-template <int MODE, int ACT>
-__device__ __forceinline__ void finish_row(uint32_t (&v)[64], const float *bias, bool has_e, uint8_t *row, int x7) {
+// The 64 columns of one accumulator row (bias added): activation, residual (or the gradient), packed
+// to bf16 into the row's 128 swizzled bytes. In LIN_GRAD p receives the unrounded values.
+template <int MODE, int ACT, bool kShare>
+__device__ __forceinline__ void finish_columns(float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ x7) << 4));
         uint4 ev = make_uint4(0u, 0u, 0u, 0u);
         if (has_e) ev = *at;
         const uint32_t ew[4] = {ev.x, ev.y, ev.z, ev.w};
-        const float4 b0 = *reinterpret_cast<const float4 *>(bias + 8 * c);
-        const float4 b1 = *reinterpret_cast<const float4 *>(bias + 8 * c + 4);
-        const float bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
         uint32_t o[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int j = 8 * c + 2 * t;
-            const float e0 = __uint_as_float(ew[t] << 16), e1 = __uint_as_float(ew[t] & 0xFFFF0000u);
-            float y0 = __uint_as_float(v[j]) + bw[2 * t], y1 = __uint_as_float(v[j + 1]) + bw[2 * t + 1];
-            if (MODE == LIN_GRAD) {
-                y0 = act_grad<ACT>(y0, e0);
-                y1 = act_grad<ACT>(y1, e1);
-                v[j] = __float_as_uint(y0);
-                v[j + 1] = __float_as_uint(y1);
-            } else {
-                y0 = act_fwd<ACT>(y0) + e0;
-                y1 = act_fwd<ACT>(y1) + e1;
-            }
-            o[t] = pack_bf16x2(y0, y1);
+            float2 &y = p[4 * c + t];
+            const float2 e = make_float2(__uint_as_float(ew[t] << 16), __uint_as_float(ew[t] & 0xFFFF0000u));
+            if (MODE == LIN_GRAD) y = act_grad2<ACT, kShare>(y, e);
+            else y = __fadd2_rn(act_fwd2<ACT, kShare>(y), e);
+            o[t] = pack_bf16x2(y.x, y.y);
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
+template <int MODE, int ACT>
+__device__ __forceinline__ void finish_row(float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
+    if (ACT == LIN_NONE || ACT == LIN_RELU || can_share(p)) finish_columns<MODE, ACT, true>(p, has_e, row, x7);
+    else finish_columns<MODE, ACT, false>(p, has_e, row, x7);
+}
+
 template <int MODE>
-__device__ __forceinline__ void finish(int act, uint32_t (&v)[64], const float *bias, bool has_e, uint8_t *row, int x7) {
-    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(v, bias, has_e, row, x7);
-    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(v, bias, has_e, row, x7);
-    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(v, bias, has_e, row, x7);
-    else finish_row<MODE, LIN_SILU>(v, bias, has_e, row, x7);
+__device__ __forceinline__ void finish(int act, float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
+    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(p, has_e, row, x7);
+    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(p, has_e, row, x7);
+    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(p, has_e, row, x7);
+    else finish_row<MODE, LIN_SILU>(p, has_e, row, x7);
 }
 
 // relu's gradient of one accumulator row: keep E where p > 0. The accumulator's rounding decides
@@ -166,16 +124,16 @@ __device__ __forceinline__ void finish(int act, uint32_t (&v)[64], const float *
 // whole of dy: where |p| is under the bound of that rounding (one step of 2^-22 of the row's
 // largest sum for each 16 products), the warp takes the row's product again in 64 bits,
 // one place at a time. At random inputs about 1 in 10^5 places.
-__device__ __forceinline__ void finish_row_relu_grad(uint32_t (&v)[64], const float *bias, uint8_t *row, int x7,
+__device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[32], const float *bias, uint8_t *row, int x7,
                                                      const LinearArgs &a, int r, int col0, int lane) {
     float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) top = fmaxf(top, fabsf(__uint_as_float(v[j])));
+    for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x - bias[2 * j]), fabsf(v[j].y - bias[2 * j + 1])));
     const float near_ = top * (float)(4 * a.kblocks + 8) * 2.384185791015625e-7f;
     uint64_t keep = 0, check = 0;
 #pragma unroll
     for (int j = 0; j < 64; ++j) {
-        const float p = __uint_as_float(v[j]) + bias[j];
+        const float p = j & 1 ? v[j >> 1].y : v[j >> 1].x;
         keep |= (uint64_t)(p > 0.f) << j;
         check |= (uint64_t)(fabsf(p) < near_) << j;
     }
@@ -207,8 +165,7 @@ __device__ __forceinline__ void finish_row_relu_grad(uint32_t (&v)[64], const fl
         for (int t = 0; t < 4; ++t) {
             const int j = 8 * c + 2 * t;
             o[t] &= ((keep >> j) & 1 ? 0xFFFFu : 0u) | ((keep >> (j + 1)) & 1 ? 0xFFFF0000u : 0u);
-            v[j] = o[t] << 16;
-            v[j + 1] = o[t] & 0xFFFF0000u;
+            v[4 * c + t] = make_float2(__uint_as_float(o[t] << 16), __uint_as_float(o[t] & 0xFFFF0000u));
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
     }
@@ -217,12 +174,13 @@ __device__ __forceinline__ void finish_row_relu_grad(uint32_t (&v)[64], const fl
 // Sums of 32 columns over the warp's 32 lanes: lane l returns column l's sum. Each step halves
 // the columns a lane holds (lanes with the bit set keep the upper half): 31 shuffles in all,
 // and the order of the additions is fixed.
-__device__ __forceinline__ float column_sum32(const uint32_t *v, int lane) {
+__device__ __forceinline__ float column_sum32(const float2 *v, int lane) {
     float s[16];
     const bool hi = (lane & 16) != 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float keep = __uint_as_float(hi ? v[i + 16] : v[i]), give = __uint_as_float(hi ? v[i] : v[i + 16]);
+        const float lo = i & 1 ? v[i >> 1].y : v[i >> 1].x, up = i & 1 ? v[(i >> 1) + 8].y : v[(i >> 1) + 8].x;
+        const float keep = hi ? up : lo, give = hi ? lo : up;
         s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
     }
 #pragma unroll
@@ -496,14 +454,19 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                     __syncwarp();
                     tmem_ld_wait_regs(v);
+                    float2 p[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        p[j] = __fadd2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                                          *reinterpret_cast<const float2 *>(mybias + ci * 64 + 2 * j));
                     if (MODE == LIN_GRAD && args.act == LIN_RELU)
-                        finish_row_relu_grad(v, mybias + ci * 64, ob + lane * 128, lane & 7, args, row0 + lane, col, lane);
+                        finish_row_relu_grad(p, mybias + ci * 64, ob + lane * 128, lane & 7, args, row0 + lane, col, lane);
                     else
-                        finish<MODE>(args.act, v, mybias + ci * 64, has_e, ob + lane * 128, lane & 7);
+                        finish<MODE>(args.act, p, has_e, ob + lane * 128, lane & 7);
                     if constexpr (MODE == LIN_GRAD) {
                         if (args.sums != nullptr) {
-                            colsum[2 * ci] += column_sum32(v, lane);
-                            colsum[2 * ci + 1] += column_sum32(v + 32, lane);
+                            colsum[2 * ci] += column_sum32(p, lane);
+                            colsum[2 * ci + 1] += column_sum32(p + 16, lane);
                         }
                     }
                 }
@@ -549,42 +512,63 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // Sums of the split products and of the column-sum partials, rounded once to bf16.
-// dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. Each thread adds its element's
-// partials in order, so the result does not depend on the launch.
+// dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. A block takes 32 places; its
+// eight warps each add every eighth partial (all loads of a lane independent), and
+// the eight sums are joined in shared memory in order: the result does not depend on
+// the launch. Up to 148 partials, bound by their reading.
 // ---------------------------------------------------------------------------
 namespace {
 
 __global__ void __launch_bounds__(256) linear_reduce_kernel(const LinearReduceArgs a) {
-    const long long quads = a.count >> 2;  // n k is a multiple of 64
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i < quads && a.dw) {
-        const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < a.splits; ++k) {
-            const float4 v = __ldcs(p + (size_t)k * quads);
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+    __shared__ float4 part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool weight = (int)blockIdx.x < a.weight_blocks;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (weight) {
+        const long long quads = a.count >> 2;  // n k is a multiple of 64
+        const long long i = (long long)blockIdx.x * 32 + lane;
+        if (i < quads) {
+            const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
+#pragma unroll 4
+            for (int k = warp; k < a.splits; k += 8) {
+                const float4 v = __ldcs(p + (size_t)k * quads);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
         }
-        reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    } else {
+        const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
+        if (j < a.n)
+#pragma unroll 4
+            for (int k = warp; k < a.sum_rows; k += 8) s.x += a.sums[(size_t)k * a.n + j];
     }
-    // Bias gradient: one warp per 32 columns in the blocks after the weight's.
-    const long long j = i - (long long)a.weight_blocks * 256;
-    if (j >= 0 && j < a.n && a.db) {
-        float s = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < a.sum_rows; ++k) s += a.sums[(size_t)k * a.n + j];
-        a.db[j] = __float2bfloat16_rn(s);
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) {
+        const float4 v = part[k][lane];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    if (weight) {
+        const long long i = (long long)blockIdx.x * 32 + lane;
+        if (i < a.count >> 2) reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    } else {
+        const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
+        if (j < a.n) a.db[j] = __float2bfloat16_rn(s.x);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s) {
-    a.weight_blocks = a.dw ? (int)((a.count / 4 + 255) / 256) : 0;
-    const int grid = a.weight_blocks + (a.db ? (a.n + 255) / 256 : 0);
+    a.weight_blocks = a.dw ? (int)((a.count / 4 + 31) / 32) : 0;
+    const int grid = a.weight_blocks + (a.db ? (a.n + 31) / 32 : 0);
     if (grid == 0) return cudaSuccess;
     linear_reduce_kernel<<<grid, 256, 0, s>>>(a);
     return cudaGetLastError();
