@@ -1255,8 +1255,12 @@ int map_operand(CUtensorMap *m, const void *t, int cols, int rows, bool mn, int 
     return map_view(m, {t, (size_t)cols, 0}, cols, rows, 1, 64, mn ? 64 : (uint32_t)tile_rows, 2,
                     CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
+// The same as blocks of 32 rows x 32 columns (64-byte rows), the drain warps' loads and stores.
 int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
-    return map_view(m, {t, (size_t)cols, 0}, cols, rows, 1, 64, 32, 2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, 1};
+    const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * 2 * rows};
+    const uint32_t box[3] = {32, 32, 1};
+    return encode(m, 3, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. Returns the groups of row tiles

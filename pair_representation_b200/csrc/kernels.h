@@ -310,7 +310,7 @@ struct LinearArgs {
 
 struct LinearMaps {
     CUtensorMap a, b;  // 64 k x 128 rows (b: BN rows), or 64 rows x 64 k when MN-major; swizzle 128B
-    CUtensorMap e, y;  // blocks of 32 rows x 128 bytes, swizzle 128B
+    CUtensorMap e, y;  // blocks of 32 rows x 32 columns: bf16 (swizzle 64B), y of LIN_WG fp32 (swizzle 128B)
 };
 
 // dw[i] = bf16(sum_s partial[s][i]), db[j] = bf16(sum_s sums[s][j]); either may be null.

@@ -18,7 +18,7 @@
 // kResident its slab of B (at most 64 KB) is loaded once and stays in shared memory;
 // only A tiles travel, through a ring. Wider contractions stream A and B together.
 // The accumulator is double-buffered in tensor memory (2 x BN columns) and drained by
-// eight warps, each storing its own 32 x 64 blocks by TMA, so the drain of one tile
+// sixteen warps, each storing its own 32 x 32 blocks by TMA, so the drain of one tile
 // overlaps the loads and MMAs of the next. E blocks arrive by TMA in the very buffer
 // the result leaves from, one block ahead.
 //
@@ -30,11 +30,11 @@ namespace trimul {
 namespace lin {
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;        // 16 KB
-constexpr int EPI_WARPS = 8;                // two per tensor-memory lane quarter
+constexpr int EPI_WARPS = 16;               // four per tensor-memory lane quarter
 constexpr int THREADS = (2 + EPI_WARPS) * 32;
-constexpr int WBUF = 4096;                  // 32 rows x 128 bytes
-constexpr int OUT_BYTES = EPI_WARPS * 2 * WBUF;
-constexpr int BIAS_BYTES = EPI_WARPS * 128 * 4;  // each drain warp's own copy of its columns' bias
+constexpr int WBUF = 4096;                  // a drain warp's: two blocks of 32 rows x 32 bf16, or one of fp32
+constexpr int OUT_BYTES = EPI_WARPS * WBUF;
+constexpr int BIAS_BYTES = EPI_WARPS * 64 * 4;  // each drain warp's own copy of its columns' bias
 constexpr int ONES_BYTES = 16 * BK * 2;     // 16 rows of ones (LIN_WG)
 constexpr int BAR_BYTES = 512;
 constexpr int RES_BYTES = 65536;            // resident slab of B
@@ -82,13 +82,13 @@ struct Tiles {
 
 namespace {
 
-// The 64 columns of one accumulator row (bias added): activation, residual (or the gradient), packed
-// to bf16 into the row's 128 swizzled bytes. In LIN_GRAD p receives the unrounded values.
+// 32 columns of one accumulator row (bias added): activation, residual (or the gradient), packed
+// to bf16 into the row's 64 swizzled bytes. In LIN_GRAD p receives the unrounded values.
 template <int MODE, int ACT, bool kShare>
-__device__ __forceinline__ void finish_columns(float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
+__device__ __forceinline__ void finish_columns(float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ x7) << 4));
+    for (int c = 0; c < 4; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ swz) << 4));
         uint4 ev = make_uint4(0u, 0u, 0u, 0u);
         if (has_e) ev = *at;
         const uint32_t ew[4] = {ev.x, ev.y, ev.z, ev.w};
@@ -106,17 +106,17 @@ __device__ __forceinline__ void finish_columns(float2 (&p)[32], bool has_e, uint
 }
 
 template <int MODE, int ACT>
-__device__ __forceinline__ void finish_row(float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
-    if (ACT == LIN_NONE || ACT == LIN_RELU || can_share(p)) finish_columns<MODE, ACT, true>(p, has_e, row, x7);
-    else finish_columns<MODE, ACT, false>(p, has_e, row, x7);
+__device__ __forceinline__ void finish_row(float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
+    if (ACT == LIN_NONE || ACT == LIN_RELU || can_share(p)) finish_columns<MODE, ACT, true>(p, has_e, row, swz);
+    else finish_columns<MODE, ACT, false>(p, has_e, row, swz);
 }
 
 template <int MODE>
-__device__ __forceinline__ void finish(int act, float2 (&p)[32], bool has_e, uint8_t *row, int x7) {
-    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(p, has_e, row, x7);
-    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(p, has_e, row, x7);
-    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(p, has_e, row, x7);
-    else finish_row<MODE, LIN_SILU>(p, has_e, row, x7);
+__device__ __forceinline__ void finish(int act, float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
+    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(p, has_e, row, swz);
+    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(p, has_e, row, swz);
+    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(p, has_e, row, swz);
+    else finish_row<MODE, LIN_SILU>(p, has_e, row, swz);
 }
 
 // relu's gradient of one accumulator row: keep E where p > 0. The accumulator's rounding decides
@@ -124,47 +124,44 @@ __device__ __forceinline__ void finish(int act, float2 (&p)[32], bool has_e, uin
 // whole of dy: where |p| is under the bound of that rounding (one step of 2^-22 of the row's
 // largest sum for each 16 products), the warp takes the row's product again in 64 bits,
 // one place at a time. At random inputs about 1 in 10^5 places.
-__device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[32], const float *bias, uint8_t *row, int x7,
+__device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[16], const float *bias, uint8_t *row, int swz,
                                                      const LinearArgs &a, int r, int col0, int lane) {
     float top = 0.f;
+    uint32_t keep = 0, check = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x - bias[2 * j]), fabsf(v[j].y - bias[2 * j + 1])));
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x - bias[2 * j]), fabsf(v[j].y - bias[2 * j + 1])));
     const float near_ = top * (float)(4 * a.kblocks + 8) * 2.384185791015625e-7f;
-    uint64_t keep = 0, check = 0;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
+    for (int j = 0; j < 32; ++j) {
         const float p = j & 1 ? v[j >> 1].y : v[j >> 1].x;
-        keep |= (uint64_t)(p > 0.f) << j;
-        check |= (uint64_t)(fabsf(p) < near_) << j;
+        keep |= (uint32_t)(p > 0.f) << j;
+        check |= (uint32_t)(fabsf(p) < near_) << j;
     }
     if (r >= a.M) check = 0;
-    if (a.N - col0 < 64) check &= (1ull << (a.N - col0)) - 1;
+    if (a.N - col0 < 32) check &= (1u << (a.N - col0)) - 1;
     for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
         const int src = __ffs(who) - 1;
         const __nv_bfloat16 *xr = a.x + (size_t)(r - lane + src) * a.K;
-        for (uint64_t left = __shfl_sync(0xffffffffu, check, src); left; left &= left - 1) {
-            const int j = __ffsll((long long)left) - 1;
+        for (uint32_t left = __shfl_sync(0xffffffffu, check, src); left; left &= left - 1) {
+            const int j = __ffs(left) - 1;
             const __nv_bfloat16 *wr = a.w + (size_t)(col0 + j) * a.K;
             double sum = 0.0;
             for (int k = lane; k < a.K; k += 32)
                 sum += (double)__bfloat162float(xr[k]) * (double)__bfloat162float(wr[k]);
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-            if (lane == src) {
-                keep &= ~(1ull << j);
-                keep |= (uint64_t)(sum + (double)bias[j] > 0.0) << j;
-            }
+            if (lane == src) keep = (keep & ~(1u << j)) | (uint32_t)(sum + (double)bias[j] > 0.0) << j;
         }
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ x7) << 4));
+    for (int c = 0; c < 4; ++c) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ swz) << 4));
         const uint4 e = *at;
         uint32_t o[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int j = 8 * c + 2 * t;
-            o[t] &= ((keep >> j) & 1 ? 0xFFFFu : 0u) | ((keep >> (j + 1)) & 1 ? 0xFFFF0000u : 0u);
+            const uint32_t two = keep >> (8 * c + 2 * t);
+            o[t] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
             v[4 * c + t] = make_float2(__uint_as_float(o[t] << 16), __uint_as_float(o[t] & 0xFFFF0000u));
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
@@ -205,8 +202,9 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     using namespace lin;
     constexpr int STAGES = stages(BN, kResident), STAGE_BYTES = stage_bytes(BN, kResident);
     constexpr int B_BYTES = BN * BK * 2;
-    constexpr int CHUNK = MODE == LIN_WG ? 32 : 64;  // accumulator columns per stored 128-byte row
-    constexpr int CHUNKS = BN / CHUNK;
+    constexpr int CHUNK = 32;                                      // accumulator columns per stored block
+    constexpr int CHUNKS = BN / CHUNK, MINE = (CHUNKS + 3) / 4;  // of a tile, and of them a drain warp's (at most)
+    constexpr int BLOCK = MODE == LIN_WG ? 4096 : 2048, BUFS = WBUF / BLOCK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem;
@@ -366,17 +364,16 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             wait_drain(drain, 0, ctl.timeout_ns);
         }
     } else {
-        // ---------------- drain warps 2..9 ----------------
-        // Warp (q, h): accumulator rows 32 q .. 32 q + 31, chunks h, h + 2, ... of each tile. Block
-        // n of this warp (counted over all its tiles) goes through buffer n & 1.
+        // ---------------- drain warps 2..17 ----------------
+        // Warp (q, h): accumulator rows 32 q .. 32 q + 31, chunks h and h + 4 of each tile. Block n of
+        // this warp (counted over all its tiles) goes through buffer n % BUFS.
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-        uint8_t *wbuf = outbuf + ew * 2 * WBUF;
+        uint8_t *wbuf = outbuf + ew * WBUF;
         uint64_t *ebar = efull + 2 * ew;
-        float *mybias = biasbuf + ew * 128;
+        float *mybias = biasbuf + ew * 64;
         const uint32_t lanebase = tmem + ((uint32_t)(q * 32) << 16);
         const bool has_e = MODE != LIN_WG && args.has_e;
-        constexpr int MINE = (CHUNKS + 1) / 2;  // chunks of a tile that are this warp's (at most)
-        float colsum[2 * MINE];
+        float colsum[MINE];
         int nst = 0, nload = 0, lt = 0;
 
         // Iterator over this warp's blocks, for the E loads that run one block ahead.
@@ -386,7 +383,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         auto load_next_e = [&]() {
             if (!ahead_ok) return;
             for (;;) {
-                ahead_c += 2;
+                ahead_c += 4;
                 if (ahead_c >= CHUNKS) {
                     if (!ahead.next()) {
                         ahead_ok = false;
@@ -399,8 +396,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                 if (col < args.N && row < args.M) {
                     if (lane == 0) {
                         tma_store_wait_read<0>();  // the block that last left from this buffer has been read
-                        mbar_arrive_expect_tx(&ebar[nload & 1], WBUF);
-                        tma_load_3d(wbuf + (nload & 1) * WBUF, &tmE, &ebar[nload & 1], col, row, 0);
+                        mbar_arrive_expect_tx(&ebar[nload & 1], BLOCK);
+                        tma_load_3d(wbuf + (nload & 1) * BLOCK, &tmE, &ebar[nload & 1], col, row, 0);
                     }
                     ++nload;
                     return;
@@ -410,14 +407,15 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         load_next_e();
         if (MODE != LIN_WG) {
             const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
-            for (int i = lane; i < 64 * MINE; i += 32) {
-                const int col = n0 + (h + 2 * (i >> 6)) * 64 + (i & 63);
-                mybias[i] = (args.bias && col < args.N) ? __bfloat162float(args.bias[col]) : 0.f;
+#pragma unroll
+            for (int i = 0; i < MINE; ++i) {
+                const int col = n0 + (h + 4 * i) * 32 + lane;
+                mybias[32 * i + lane] = (args.bias && col < args.N) ? __bfloat162float(args.bias[col]) : 0.f;
             }
             __syncwarp();
         }
 #pragma unroll
-        for (int i = 0; i < 2 * MINE; ++i) colsum[i] = 0.f;
+        for (int i = 0; i < MINE; ++i) colsum[i] = 0.f;
         bool ok = true;
         Tiles<MODE> t(args);
         while (ok && t.next()) {
@@ -427,48 +425,40 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             const int row0 = t.rt * BM + 32 * q;
 #pragma unroll
             for (int ci = 0; ci < MINE; ++ci) {
-                const int ch = h + 2 * ci, col = t.ct * BN + ch * CHUNK;
+                const int ch = h + 4 * ci, col = t.ct * BN + ch * CHUNK;
                 if (ch >= CHUNKS || row0 >= args.M || col >= args.N) continue;
-                uint8_t *ob = wbuf + (nst & 1) * WBUF;
+                uint8_t *ob = wbuf + (nst % BUFS) * BLOCK;
                 const uint32_t taddr = lanebase + (uint32_t)(acc * BN + ch * CHUNK);
+                uint32_t v[32];
+                tmem_ld32(taddr, v);
+                if (has_e) {
+                    load_next_e();
+                    if (!(ok = warp_wait(&ebar[nst & 1], (uint32_t)(nst >> 1) & 1u, abort_flag, ctl, SITE_LIN | 7, t.rt)))
+                        break;
+                } else if (lane == 0) {
+                    tma_store_wait_read<BUFS - 1>();
+                }
+                __syncwarp();
+                tmem_ld_wait_regs(v);
                 if constexpr (MODE == LIN_WG) {
-                    uint32_t v[32];
-                    tmem_ld32(taddr, v);
-                    if (lane == 0) tma_store_wait_read<1>();
-                    __syncwarp();
-                    tmem_ld_wait_regs(v);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         *reinterpret_cast<uint4 *>(ob + lane * 128 + ((c ^ (lane & 7)) << 4)) =
                             make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                 } else {
-                    uint32_t v[64];
-                    tmem_ld32(taddr, v);
-                    tmem_ld32(taddr + 32, v + 32);
-                    if (has_e) {
-                        load_next_e();
-                        if (!(ok = warp_wait(&ebar[nst & 1], (uint32_t)(nst >> 1) & 1u, abort_flag, ctl, SITE_LIN | 7, t.rt)))
-                            break;
-                    } else if (lane == 0) {
-                        tma_store_wait_read<1>();
-                    }
-                    __syncwarp();
-                    tmem_ld_wait_regs(v);
-                    float2 p[32];
+                    const float *bias = mybias + 32 * ci;
+                    float2 p[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 16; ++j)
                         p[j] = __fadd2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                                          *reinterpret_cast<const float2 *>(mybias + ci * 64 + 2 * j));
+                                          *reinterpret_cast<const float2 *>(bias + 2 * j));
+                    uint8_t *row = ob + lane * 64;
+                    const int swz = (lane >> 1) & 3;
                     if (MODE == LIN_GRAD && args.act == LIN_RELU)
-                        finish_row_relu_grad(p, mybias + ci * 64, ob + lane * 128, lane & 7, args, row0 + lane, col, lane);
+                        finish_row_relu_grad(p, bias, row, swz, args, row0 + lane, col, lane);
                     else
-                        finish<MODE>(args.act, p, has_e, ob + lane * 128, lane & 7);
-                    if constexpr (MODE == LIN_GRAD) {
-                        if (args.sums != nullptr) {
-                            colsum[2 * ci] += column_sum32(p, lane);
-                            colsum[2 * ci + 1] += column_sum32(p + 16, lane);
-                        }
-                    }
+                        finish<MODE>(args.act, p, has_e, row, swz);
+                    if (MODE == LIN_GRAD && args.sums != nullptr) colsum[ci] += column_sum32(p, lane);
                 }
                 ++nst;
                 fence_proxy_async_smem();
@@ -494,8 +484,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         if (MODE == LIN_GRAD && args.sums != nullptr) {
             float *dst = args.sums + (size_t)(((int)blockIdx.x / args.col_tiles) * 4 + q) * args.N;
 #pragma unroll
-            for (int i = 0; i < 2 * MINE; ++i) {
-                const int ch = h + 2 * (i >> 1), col = ((int)blockIdx.x % args.col_tiles) * BN + ch * 64 + 32 * (i & 1) + lane;
+            for (int i = 0; i < MINE; ++i) {
+                const int ch = h + 4 * i, col = ((int)blockIdx.x % args.col_tiles) * BN + ch * 32 + lane;
                 if (ch < CHUNKS && col < args.N) dst[col] = colsum[i];
             }
         }
