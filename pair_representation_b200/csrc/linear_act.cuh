@@ -2,11 +2,11 @@
 //
 // exp(-p) and 1 / (1 + exp(-p)) come from the hardware's ex2 and rcp (relative errors about
 // 2^-22), far under the half step 2^-8 of the bf16 result. Those run at 16 a clock and SM, and at
-// two for each value they, not memory, bound a wide layer's epilogue (589824 x 128 -> 512 with
-// silu: 226 us, without activation 128). So two values share one reciprocal,
-//   1 / a = b / (a b),  1 / b = a / (a b),
-// which takes 1.5 for each. The product stays finite while both p are over -43; where one of the
-// them is not, or is NaN, each takes its own.
+// two for each value they and the arithmetic around them, not memory, bound a wide layer's epilogue
+// (589824 x 128 -> 512 with silu: 226 us, without activation 128). So four values share one
+// reciprocal: of a b c d, times c d and then b it is 1 / a, and so on; 1.25 for each, and fewer
+// instructions too. The product stays finite while all four p are over -21; where one of the values a
+// thread has in hand is not, or is NaN, each takes its own.
 #pragma once
 
 #include "kernels.h"
@@ -34,27 +34,34 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// Whether pairs of these may share a reciprocal (false with a NaN among them). Asked once for all the
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Whether these may share reciprocals (false with a NaN among them). Asked once for all the
 // values a thread has in hand: a test and branch for every eight kept the two warps of a scheduler
 // from having enough exponentials in flight (286 us in the case above).
 template <int N>
 __device__ __forceinline__ bool can_share(const float2 (&p)[N]) {
-    float m[4] = {p[0].x, p[0].y, p[1].x, p[1].y};
+    float m[2] = {p[0].x, p[0].y};
 #pragma unroll
-    for (int t = 2; t < N; ++t) {
-        m[(2 * t) & 3] = min_nan(m[(2 * t) & 3], p[t].x);
-        m[(2 * t + 1) & 3] = min_nan(m[(2 * t + 1) & 3], p[t].y);
-    }
-    return min_nan(min_nan(m[0], m[1]), min_nan(m[2], m[3])) >= -43.f;
+    for (int t = 1; t < N; ++t) m[t & 1] = min3_nan(m[t & 1], p[t].x, p[t].y);
+    return min_nan(m[0], m[1]) >= -21.f;
 }
 
-// e = exp(-p) and 1 / (1 + e) of two values over -43.
-__device__ __forceinline__ float2 sigmoid_shared(float2 p, float2 &e) {
-    const float2 z = __fmul2_rn(p, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    e = make_float2(ex2f(z.x), ex2f(z.y));
-    const float2 a = __fadd2_rn(e, make_float2(1.f, 1.f));
-    const float r = rcpf(a.x * a.y);
-    return __fmul2_rn(make_float2(r, r), make_float2(a.y, a.x));
+// 1 / (1 + exp(-p)) of four values over -21; e receives the exponentials.
+__device__ __forceinline__ void sigmoid_shared(const float2 (&p)[2], float2 (&s)[2], float2 (&e)[2]) {
+    const float2 l = make_float2(-1.4426950408889634f, -1.4426950408889634f), one = make_float2(1.f, 1.f);
+    const float2 y = __fmul2_rn(p[0], l), z = __fmul2_rn(p[1], l);
+    e[0] = make_float2(ex2f(y.x), ex2f(y.y));
+    e[1] = make_float2(ex2f(z.x), ex2f(z.y));
+    const float2 a = __fadd2_rn(e[0], one), c = __fadd2_rn(e[1], one), ac = __fmul2_rn(a, c);
+    const float r = rcpf(ac.x * ac.y);
+    const float2 t = make_float2(r * ac.y, r * ac.x);  // 1 / (a.x c.x), 1 / (a.y c.y)
+    s[0] = __fmul2_rn(t, c);
+    s[1] = __fmul2_rn(t, a);
 }
 
 template <int ACT>
@@ -72,25 +79,36 @@ __device__ __forceinline__ float act_grad(float p, float d) {
     return ACT == LIN_SIGMOID ? d * (s * c) : d * fmaf(p * s, c, s);
 }
 
-// Two values: act(p), and act'(p) d (not relu's, whose sign may need more than fp32: see its own
-// code). kShare: can_share holds.
+// Four values: p = act(p), and p = act'(p) d (not relu's, whose sign may need more than fp32: see its
+// own code). kShare: can_share holds.
 template <int ACT, bool kShare>
-__device__ __forceinline__ float2 act_fwd2(float2 p) {
-    if (ACT == LIN_NONE) return p;
-    if (ACT == LIN_RELU) return make_float2(max_nan(p.x, 0.f), max_nan(p.y, 0.f));
-    if (!kShare) return make_float2(act_fwd<ACT>(p.x), act_fwd<ACT>(p.y));
-    float2 e;
-    const float2 s = sigmoid_shared(p, e);
-    return ACT == LIN_SIGMOID ? s : __fmul2_rn(p, s);
+__device__ __forceinline__ void act_fwd4(float2 (&p)[2]) {
+    if (ACT == LIN_NONE) return;
+    float2 s[2], e[2];
+    if (ACT != LIN_RELU && kShare) sigmoid_shared(p, s, e);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        if (ACT == LIN_RELU) p[t] = make_float2(max_nan(p[t].x, 0.f), max_nan(p[t].y, 0.f));
+        else if (!kShare) p[t] = make_float2(act_fwd<ACT>(p[t].x), act_fwd<ACT>(p[t].y));
+        else p[t] = ACT == LIN_SIGMOID ? s[t] : __fmul2_rn(p[t], s[t]);
+    }
 }
 
 template <int ACT, bool kShare>
-__device__ __forceinline__ float2 act_grad2(float2 p, float2 d) {
-    if (ACT == LIN_NONE) return d;
-    if (!kShare) return make_float2(act_grad<ACT>(p.x, d.x), act_grad<ACT>(p.y, d.y));
-    float2 e;
-    const float2 s = sigmoid_shared(p, e), c = __fmul2_rn(s, e);
-    return __fmul2_rn(d, ACT == LIN_SIGMOID ? __fmul2_rn(s, c) : __ffma2_rn(__fmul2_rn(p, s), c, s));
+__device__ __forceinline__ void act_grad4(float2 (&p)[2], const float2 (&d)[2]) {
+    float2 s[2], e[2];
+    if (ACT != LIN_NONE && kShare) sigmoid_shared(p, s, e);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        if (ACT == LIN_NONE) {
+            p[t] = d[t];
+        } else if (!kShare) {
+            p[t] = make_float2(act_grad<ACT>(p[t].x, d[t].x), act_grad<ACT>(p[t].y, d[t].y));
+        } else {
+            const float2 c = __fmul2_rn(s[t], e[t]);
+            p[t] = __fmul2_rn(d[t], ACT == LIN_SIGMOID ? __fmul2_rn(s[t], c) : __ffma2_rn(__fmul2_rn(p[t], s[t]), c, s[t]));
+        }
+    }
 }
 
 }  // namespace trimul

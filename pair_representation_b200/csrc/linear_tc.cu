@@ -84,39 +84,46 @@ namespace {
 
 // 32 columns of one accumulator row (bias added): activation, residual (or the gradient), packed
 // to bf16 into the row's 64 swizzled bytes. In LIN_GRAD p receives the unrounded values.
-template <int MODE, int ACT, bool kShare>
-__device__ __forceinline__ void finish_columns(float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
+template <int MODE, int ACT, bool kShare, bool kE>
+__device__ __forceinline__ void finish_columns(float2 (&p)[16], uint8_t *row, int swz) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint4 *at = reinterpret_cast<uint4 *>(row + ((c ^ swz) << 4));
         uint4 ev = make_uint4(0u, 0u, 0u, 0u);
-        if (has_e) ev = *at;
+        if (kE) ev = *at;
         const uint32_t ew[4] = {ev.x, ev.y, ev.z, ev.w};
         uint32_t o[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            float2 &y = p[4 * c + t];
-            const float2 e = make_float2(__uint_as_float(ew[t] << 16), __uint_as_float(ew[t] & 0xFFFF0000u));
-            if (MODE == LIN_GRAD) y = act_grad2<ACT, kShare>(y, e);
-            else y = __fadd2_rn(act_fwd2<ACT, kShare>(y), e);
-            o[t] = pack_bf16x2(y.x, y.y);
+        for (int t = 0; t < 4; t += 2) {
+            float2 e[2], y[2] = {p[4 * c + t], p[4 * c + t + 1]};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                e[u] = make_float2(__uint_as_float(ew[t + u] << 16), __uint_as_float(ew[t + u] & 0xFFFF0000u));
+            if (MODE == LIN_GRAD) act_grad4<ACT, kShare>(y, e);
+            else act_fwd4<ACT, kShare>(y);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (MODE == LIN_FWD && kE) y[u] = __fadd2_rn(y[u], e[u]);
+                if (MODE == LIN_GRAD) p[4 * c + t + u] = y[u];
+                o[t + u] = pack_bf16x2(y[u].x, y[u].y);
+            }
         }
         *at = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-template <int MODE, int ACT>
-__device__ __forceinline__ void finish_row(float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
-    if (ACT == LIN_NONE || ACT == LIN_RELU || can_share(p)) finish_columns<MODE, ACT, true>(p, has_e, row, swz);
-    else finish_columns<MODE, ACT, false>(p, has_e, row, swz);
+template <int MODE, int ACT, bool kE>
+__device__ __forceinline__ void finish_row(float2 (&p)[16], uint8_t *row, int swz) {
+    if (ACT == LIN_NONE || ACT == LIN_RELU || can_share(p)) finish_columns<MODE, ACT, true, kE>(p, row, swz);
+    else finish_columns<MODE, ACT, false, kE>(p, row, swz);
 }
 
-template <int MODE>
-__device__ __forceinline__ void finish(int act, float2 (&p)[16], bool has_e, uint8_t *row, int swz) {
-    if (act == LIN_NONE) finish_row<MODE, LIN_NONE>(p, has_e, row, swz);
-    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU>(p, has_e, row, swz);
-    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID>(p, has_e, row, swz);
-    else finish_row<MODE, LIN_SILU>(p, has_e, row, swz);
+template <int MODE, bool kE>
+__device__ __forceinline__ void finish(int act, float2 (&p)[16], uint8_t *row, int swz) {
+    if (act == LIN_NONE) finish_row<MODE, LIN_NONE, kE>(p, row, swz);
+    else if (MODE == LIN_FWD && act == LIN_RELU) finish_row<MODE, LIN_RELU, kE>(p, row, swz);
+    else if (act == LIN_SIGMOID) finish_row<MODE, LIN_SIGMOID, kE>(p, row, swz);
+    else finish_row<MODE, LIN_SILU, kE>(p, row, swz);
 }
 
 // relu's gradient of one accumulator row: keep E where p > 0. The accumulator's rounding decides
@@ -456,8 +463,10 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     const int swz = (lane >> 1) & 3;
                     if (MODE == LIN_GRAD && args.act == LIN_RELU)
                         finish_row_relu_grad(p, bias, row, swz, args, row0 + lane, col, lane);
+                    else if (MODE == LIN_GRAD || has_e)
+                        finish<MODE, true>(args.act, p, row, swz);
                     else
-                        finish<MODE>(args.act, p, has_e, row, swz);
+                        finish<MODE, false>(args.act, p, row, swz);
                     if (MODE == LIN_GRAD && args.sums != nullptr) colsum[ci] += column_sum32(p, lane);
                 }
                 ++nst;
