@@ -19,7 +19,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libtrimul_b200.so")
 SOURCES = ["api.cu", "prologue_tc.cu", "contract_tc.cu", "epilogue_tc.cu", "simt_f32.cu", "noalloc.cu",
            "backward.cu", "atomattn_tc.cu", "mx_tc.cu", "atomattn_bwd.cu", "linear_tc.cu",
-           "act8.cu"]
+           "linear_bwd_tc.cu", "act8.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tile_ops.cuh", "mx_block.cuh", "linear_act.cuh"]
 
 
@@ -45,7 +45,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "-ldl",
+           "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-cudart", "static", "-ldl",
            "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp]
     if ptxas_verbose:
         cmd += ["-Xptxas", "-v"]

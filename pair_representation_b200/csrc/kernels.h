@@ -331,6 +331,44 @@ bool linear_resident(int bn, int kblocks);
 cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, cudaStream_t s);
 cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s);
 
+// ---- the backward in one pass, in_features <= 128 (linear_bwd_tc.cu) ---------------
+
+enum LinearBwdDx {
+    LBW_DX_NONE = 0,  // not wanted
+    LBW_DX_BF16 = 1,  // written
+    LBW_DX_PART = 2,  // written to dx_part in fp32
+    LBW_DX_ADD = 3,   // added to dx_part and written
+};
+
+struct LinearBwdArgs {
+    long long rows;
+    int row_tiles;  // of 128 rows
+    int k, n;       // k <= 128; n <= 256: columns of dy that this launch takes
+    int act;
+    const __nv_bfloat16 *bias;  // [n] or null
+    const uint8_t *scales;      // x in 8 bits: [rows][k / 32], else null
+    int dx_mode;
+    float *dx_part;  // [rows][k]
+    int has_dw, has_db;
+    float *partial;  // [grid][part_stride]: dW [n][k] of each CTA, unless dw_out
+    long long part_stride;
+    __nv_bfloat16 *dw_out;  // [n][k], one CTA
+    float *sums;            // [grid][sums_stride]: db of each CTA, unless db_out
+    int sums_stride;
+    __nv_bfloat16 *db_out;  // [n], one CTA
+    int clear_status;
+    KernelCtl ctl;
+};
+
+struct LinearBwdMaps {
+    CUtensorMap x;      // boxes 64 columns x 128 rows, swizzle 128B; in 8 bits: 128 bytes x 128 rows
+    CUtensorMap w, dy;  // boxes 64 columns x 128 rows, swizzle 128B
+    CUtensorMap dx;     // boxes 32 columns x 32 rows, swizzle 64B
+};
+
+cudaError_t linear_bwd_setup();
+cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int grid, cudaStream_t s);
+
 // ---- activations in 8 bits (act8.cu); values: a multiple of 32 -------------------
 
 cudaError_t launch_act8_pack(const void *x, void *codes, void *scales, long long values, int sms, cudaStream_t s);

@@ -1,0 +1,584 @@
+// linear_bwd_tc.cu - the whole backward of a linear layer up to 128 wide on the input side in one
+// pass over the batch, on tcgen05 tensor cores.
+//
+//   p = x W^T + b,  D = dy act'(p),  dx = D W,  dW = D^T x,  db = sum of D over the rows
+//
+// What bounds it: memory. A row of x, dy and dx is 2 (2 k + n) bytes; done as three products with
+// D in memory it is read and written 2.3 times over (147456 x 128 -> 128 with sigmoid: 79 us). Here a
+// CTA takes tiles of 128 rows, and from one copy of x and dy in shared memory makes all of it:
+//   * W (up to 256 rows of it) stays in shared memory for the whole call, left in the one
+//     layout that serves both as the right operand of p (K-major) and of dx (MN-major);
+//   * per tile and 128 columns of n: p in tensor memory; sixteen worker warps turn dy into D
+//     in place (the tile it arrived in); D is then the K-major left operand of dx and the
+//     MN-major left operand of dW, x the MN-major right operand of dW, all as they lie;
+//   * dx leaves tensor memory once per tile; dW stays there as a running sum over all the CTA's
+//     tiles (128 or 256 columns) and is written once, in fp32, for linear_reduce_kernel to add up
+//     the CTAs' parts in order; db likewise, summed from D before its rounding.
+// n over 256: one call per 256 columns of n, dx passing between them in fp32.
+// kHeld8: x comes as E4M3 codes and E8M0 scales; the workers turn each tile into bf16 as it
+// arrives, so the 8-bit form is all that is read.
+//
+// The workers read p in the 16 x 256-bit fragment form, so ldmatrix and stmatrix meet it in the
+// swizzled tile without conflicts, and a lane's part of db is eight columns: it adds its rows in
+// registers, tile after tile, and the lanes are joined once, at the end.
+//
+// Roles: warp 0 TMA, warp 1 MMA issue, warps 2-17 workers. Every wait is bounded; see the barrier
+// list below. Order within a tile, so that no role waits on itself: the MMA warp issues p of
+// the next unit before it waits for D of this one (kHeld8: not across tiles, where x is still read),
+// and dW of a unit before dx, which may wait for the drain of the tile before; the workers drain
+// that after the tile's first unit.
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "linear_act.cuh"
+
+namespace trimul {
+namespace lb {
+constexpr int TILE = 128 * 128 * 2;       // 128 rows x 128 columns of bf16: two blocks of 64 columns
+constexpr int HALF = TILE / 2;
+constexpr int WORKERS = 16;
+constexpr int THREADS = (2 + WORKERS) * 32;
+constexpr int CODES = 128 * 128;          // a tile's codes
+constexpr int OUT = 32 * 64;              // a worker's block of dx: 32 rows x 32 columns
+constexpr int BAR_BYTES = 256;
+__host__ __device__ constexpr size_t smem(int chunks) {
+    // W, x (two tiles; kHeld8: one, and two of codes), D (two), dx blocks, bias and db sums
+    return 1024 + (size_t)chunks * TILE + 2 * TILE + 2 * TILE + WORKERS * OUT + 1024 + BAR_BYTES;
+}
+static_assert(smem(2) <= 232448, "shared memory budget");
+constexpr int TMEM_COLS = 512, DX_COL = 384;
+}  // namespace lb
+
+namespace {
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ float2 two(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+// Four bf16 at column 4 l of row r of a 128 x 128 tile.
+__device__ __forceinline__ uint2 tile_quad(const uint8_t *tile, int r, int l) {
+    return *reinterpret_cast<const uint2 *>(tile + (l >> 4) * lb::HALF + r * 128 + ((((l & 15) >> 1) ^ (r & 7)) << 4) + (l & 1) * 8);
+}
+
+}  // namespace
+
+template <int CHUNKS, bool kHeld8, int ACT>
+__global__ void __launch_bounds__(lb::THREADS, 1)
+    linear_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmDx,
+                      const LinearBwdArgs args) {
+    using namespace lb;
+    constexpr int PRE = CHUNKS == 1 ? 2 : 1;     // accumulators of p
+    constexpr int PRE_COL = 128 * CHUNKS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *wbuf = smem;                               // [CHUNKS] 128 rows of W
+    uint8_t *xbuf = wbuf + CHUNKS * TILE;               // kHeld8: one tile, else two
+    uint8_t *codes = xbuf + TILE;                       // kHeld8: [2]
+    uint8_t *dbuf = xbuf + 2 * TILE;                    // [2] dy, then D
+    uint8_t *obuf = dbuf + 2 * TILE;                    // [WORKERS]
+    float *fbuf = reinterpret_cast<float *>(obuf + WORKERS * OUT);  // bias [256]; at the end db sums
+    uint64_t *bars = reinterpret_cast<uint64_t *>(fbuf + 256);
+    uint64_t *wfull = bars;            // W landed
+    uint64_t *xfull = bars + 1;        // [2] x (kHeld8: codes) landed
+    uint64_t *xready = bars + 3;       // kHeld8: x turned into bf16 (WORKERS arrivals)
+    uint64_t *cfree = bars + 4;        // kHeld8: [2] codes read (WORKERS arrivals)
+    uint64_t *xfree = bars + 6;        // [2] products reading x are done
+    uint64_t *dfull = bars + 8;        // [2] dy landed
+    uint64_t *dready = bars + 10;      // [2] D written (WORKERS arrivals)
+    uint64_t *dfree = bars + 12;       // [2] products reading D are done
+    uint64_t *pfull = bars + 14;       // [2] p complete
+    uint64_t *pfree = bars + 16;       // [2] p read (WORKERS arrivals)
+    uint64_t *dxfull = bars + 18;      // dx of a tile complete
+    uint64_t *dxfree = bars + 19;      // dx read (WORKERS arrivals)
+    uint64_t *drain = bars + 20;       // every product is done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 21);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const KernelCtl &ctl = args.ctl;
+    const int my_tiles = ((int)args.row_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int units = my_tiles * CHUNKS;
+    constexpr bool has_p = ACT != LIN_NONE;
+    auto row0 = [&](int t) { return ((int)blockIdx.x + t * (int)gridDim.x) * 128; };
+
+    if (threadIdx.x == 0) {
+        mbar_init(wfull, 1);
+        mbar_init(xready, WORKERS);
+        mbar_init(dxfull, 1);
+        mbar_init(dxfree, WORKERS);
+        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&xfull[i], 1);
+            mbar_init(&cfree[i], WORKERS);
+            mbar_init(&xfree[i], 1);
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dready[i], WORKERS);
+            mbar_init(&dfree[i], 1);
+            mbar_init(&pfull[i], 1);
+            mbar_init(&pfree[i], WORKERS);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmDy);
+        if (args.dx_mode == LBW_DX_BF16 || args.dx_mode == LBW_DX_ADD) tma_prefetch_desc(&tmDx);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    for (int i = threadIdx.x; i < 128 * CHUNKS; i += THREADS)
+        fbuf[i] = (args.bias && i < args.n) ? __bfloat162float(args.bias[i]) : 0.f;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
+
+    // Workers keep these across their branch: db of their columns.
+    float2 dbs[CHUNKS][4];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dbs[c][j] = make_float2(0.f, 0.f);
+    const int ew = warp - 2, q = warp & 3, h = ew >> 2;  // worker: rows 32 q .., columns 32 h .. of a tile
+    const uint32_t lanebase = tmem + ((uint32_t)(q * 32) << 16);
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA ----------------
+            int xs = 0, ds = 0;  // tiles of x and units of dy asked for
+            mbar_arrive_expect_tx(wfull, CHUNKS * TILE);
+            for (int c = 0; c < CHUNKS; ++c)
+                for (int kb = 0; kb < 2; ++kb) tma_load_3d(wbuf + c * TILE + kb * HALF, &tmW, wfull, kb * 64, c * 128, 0);
+            for (int u = 0; ok && u < units; ++u) {
+                const int t = u / CHUNKS, c = u - t * CHUNKS;
+                if (c == 0) {
+                    const int xb = t & 1;
+                    uint64_t *fr = kHeld8 ? &cfree[xb] : &xfree[xb];
+                    if (t >= 2 && !(ok = wait_bounded(fr, (uint32_t)((t >> 1) - 1) & 1u, abort_flag, ctl, SITE_LBW | 1, t))) break;
+                    if (kHeld8) {
+                        mbar_arrive_expect_tx(&xfull[xb], CODES);
+                        tma_load_3d(codes + xb * CODES, &tmX, &xfull[xb], 0, row0(t), 0);
+                    } else {
+                        mbar_arrive_expect_tx(&xfull[xb], TILE);
+                        for (int kb = 0; kb < 2; ++kb)
+                            tma_load_3d(xbuf + xb * TILE + kb * HALF, &tmX, &xfull[xb], kb * 64, row0(t), 0);
+                    }
+                    ++xs;
+                }
+                const int db = u & 1;
+                if (u >= 2 && !(ok = wait_bounded(&dfree[db], (uint32_t)((u >> 1) - 1) & 1u, abort_flag, ctl, SITE_LBW | 2, u))) break;
+                mbar_arrive_expect_tx(&dfull[db], TILE);
+                for (int nb = 0; nb < 2; ++nb)
+                    tma_load_3d(dbuf + db * TILE + nb * HALF, &tmDy, &dfull[db], c * 128 + nb * 64, row0(t), 0);
+                ++ds;
+            }
+            // No copy may be in flight when the CTA leaves.
+            wait_drain(wfull, 0, ctl.timeout_ns);
+            for (int i = 0; i < 2; ++i) {
+                const int nx = (xs + 1 - i) / 2, nd = (ds + 1 - i) / 2;  // phases of buffer i
+                if (nx > 0) wait_drain(&xfull[i], (uint32_t)(nx - 1) & 1u, ctl.timeout_ns);
+                if (nd > 0) wait_drain(&dfull[i], (uint32_t)(nd - 1) & 1u, ctl.timeout_ns);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issue ----------------
+            const uint32_t i_p = idesc_bf16(128, 128, 0, 0), i_dx = idesc_bf16(128, 128, 0, 1), i_dw = idesc_bf16(128, 128, 1, 1);
+            const uint32_t w0 = smem_u32(wbuf), x0 = smem_u32(xbuf), d0 = smem_u32(dbuf);
+            ok = wait_bounded(wfull, 0, abort_flag, ctl, SITE_LBW | 3, 0);
+            auto xtile = [&](int t) { return x0 + (kHeld8 ? 0u : (uint32_t)((t & 1) * TILE)); };
+            auto wait_x = [&](int t) {
+                if (kHeld8) return wait_bounded(xready, (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 4, t);
+                return wait_bounded(&xfull[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 4, t);
+            };
+            // p of unit u, once x is there and the accumulator has been read.
+            auto issue_p = [&](int u) {
+                const int t = u / CHUNKS, c = u - t * CHUNKS, a = u % PRE;
+                if (c == 0 && !wait_x(t)) return false;
+                if (u >= PRE && !wait_bounded(&pfree[a], (uint32_t)(u / PRE - 1) & 1u, abort_flag, ctl, SITE_LBW | 5, u)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    mma_bf16(tmem + PRE_COL + 128 * a, sdesc_sw128(xtile(t) + (j >> 2) * HALF + (j & 3) * 32, 16, 1024),
+                             sdesc_sw128(w0 + c * TILE + (j >> 2) * HALF + (j & 3) * 32, 16, 1024), i_p, j ? 1u : 0u);
+                mma_commit(&pfull[a]);
+                return true;
+            };
+            if (ok && has_p && units > 0) ok = issue_p(0);
+            for (int u = 0; ok && u < units; ++u) {
+                const int t = u / CHUNKS, c = u - t * CHUNKS, db = u & 1;
+                const bool wait_for_x = kHeld8 && c == CHUNKS - 1;  // the next p needs x's tile, which dW here still reads
+                if (has_p && u + 1 < units && !wait_for_x && !(ok = issue_p(u + 1))) break;
+                if (!has_p && c == 0 && !(ok = wait_x(t))) break;
+                if (!(ok = wait_bounded(&dready[db], (uint32_t)(u >> 1) & 1u, abort_flag, ctl, SITE_LBW | 6, u))) break;
+                tc_fence_after();
+                const uint32_t dt = d0 + db * TILE;
+                if (args.has_dw) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mma_bf16(tmem + 128 * c, sdesc_sw128(dt + j * 2048, HALF, 1024), sdesc_sw128(xtile(t) + j * 2048, HALF, 1024),
+                                 i_dw, (t | j) ? 1u : 0u);
+                }
+                if (args.dx_mode != LBW_DX_NONE) {
+                    if (c == 0 && t > 0) {
+                        if (!(ok = wait_bounded(dxfree, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 7, t))) break;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        mma_bf16(tmem + DX_COL, sdesc_sw128(dt + (j >> 2) * HALF + (j & 3) * 32, 16, 1024),
+                                 sdesc_sw128(w0 + c * TILE + j * 2048, HALF, 1024), i_dx, (c | j) ? 1u : 0u);
+                }
+                mma_commit(&dfree[db]);
+                if (c == CHUNKS - 1) {
+                    mma_commit(&xfree[kHeld8 ? 0 : t & 1]);
+                    mma_commit(dxfull);
+                }
+                if (has_p && u + 1 < units && wait_for_x && !(ok = issue_p(u + 1))) break;
+            }
+            mma_commit(drain);
+            wait_drain(drain, 0, ctl.timeout_ns);
+        }
+    } else {
+        // ---------------- workers ----------------
+        const uint32_t la_off = (uint32_t)((32 * q + (lane & 7) + ((lane >> 3) & 1) * 8) * 128);  // row of an ldmatrix address
+        const int la_c = lane >> 4, x7 = lane & 7;
+        uint8_t *ob = obuf + ew * OUT;
+        // kHeld8: thread (row, 32-column block) of the conversion
+        const int crow = ew * 8 + (lane >> 2), cblk = lane & 3, kblk = args.k >> 5;
+
+        auto scale_of = [&](int t) -> uint32_t {
+            const long long r = (long long)row0(t) + crow;
+            return (kHeld8 && t < my_tiles && r < args.rows && cblk < kblk) ? (uint32_t)__ldg(args.scales + r * kblk + cblk) : 0u;
+        };
+        uint32_t scale_next = kHeld8 ? scale_of(0) : 0u;
+        auto convert = [&](int t) {
+            if (!warp_wait(&xfull[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 8, t)) return false;
+            if (t > 0 && !warp_wait(&xfree[0], (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 9, t)) return false;
+            const uint32_t s = scale_next;
+            scale_next = scale_of(t + 1);
+            const float size = __uint_as_float(s ? s << 23 : 0x00400000u);  // 2^(s - 127)
+            const uint8_t *src = codes + (t & 1) * CODES + crow * 128;
+            uint8_t *dst = xbuf + (cblk >> 1) * HALF + crow * 128;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + (((2 * cblk + i) ^ (crow & 7)) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hv));
+                    o[j] = pack_bf16x2(f.x * size, f.y * size);
+                }
+                const int ch = 4 * (cblk & 1) + 2 * i;
+                *reinterpret_cast<uint4 *>(dst + ((ch ^ (crow & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (crow & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&cfree[t & 1]);
+                mbar_arrive(xready);
+            }
+            return true;
+        };
+
+        // D of unit u in place of dy; db of its columns.
+        auto make_d = [&](int u) {
+            const int t = u / CHUNKS, c = u - t * CHUNKS, a = u % PRE, db = u & 1;
+            float2 p[16];  // [16-row half][8-column block][row, row + 8]
+            if (has_p) {
+                if (!warp_wait(&pfull[a], (uint32_t)(u / PRE) & 1u, abort_flag, ctl, SITE_LBW | 10, u)) return false;
+                tc_fence_after();
+                uint32_t v[2][16];
+#pragma unroll
+                for (int rh = 0; rh < 2; ++rh)
+                    tmem_ld16x256_x4(lanebase + ((uint32_t)(16 * rh) << 16) + (uint32_t)(PRE_COL + 128 * a + 32 * h), v[rh]);
+                tmem_ld_wait_regs(v[0]);
+                tmem_ld_wait_regs(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfree[a]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 bv = *reinterpret_cast<const float2 *>(fbuf + c * 128 + 32 * h + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float2 &y = p[(x >> 1) * 8 + 2 * j + (x & 1)];
+                        const uint32_t *r = &v[x >> 1][4 * j + 2 * (x & 1)];
+                        y = __fadd2_rn(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])), bv);
+                    }
+                }
+            }
+            if (!warp_wait(&dfull[db], (uint32_t)(u >> 1) & 1u, abort_flag, ctl, SITE_LBW | 11, u)) return false;
+            const uint32_t tile = smem_u32(dbuf + db * TILE + (h >> 1) * HALF) + la_off;
+            uint32_t keep = 0xFFFFFFFFu;  // relu: bit 2 i + e of value p[i].x or .y
+            if (ACT == LIN_RELU) {
+                // The sign of a p next to 0 is taken again in 64 bits (see linear_tc.cu).
+                float top = 0.f;
+                uint32_t check = 0;
+                keep = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(p[i].x), fabsf(p[i].y)));
+                const float near_ = top * (16.f * 2.384185791015625e-7f);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    keep |= ((p[i].x > 0.f ? 1u : 0u) | (p[i].y > 0.f ? 2u : 0u)) << (2 * i);
+                    check |= ((fabsf(p[i].x) < near_ ? 1u : 0u) | (fabsf(p[i].y) < near_ ? 2u : 0u)) << (2 * i);
+                }
+                if (__any_sync(0xffffffffu, check != 0)) {
+                    // x and W are read here as they landed: observe their barriers.
+                    uint64_t *xb = kHeld8 ? xready : &xfull[t & 1];
+                    if (!warp_wait(wfull, 0, abort_flag, ctl, SITE_LBW | 14, u) ||
+                        !warp_wait(xb, (uint32_t)(kHeld8 ? t : t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 14, u))
+                        return false;
+                }
+                for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
+                    const int src = __ffs(who) - 1;
+                    for (uint32_t left = __shfl_sync(0xffffffffu, check, src); left; left &= left - 1) {
+                        const int bit = __ffs(left) - 1, i = bit >> 1;
+                        const int r = 32 * q + 16 * (i >> 3) + 8 * (i & 1) + (src >> 2);
+                        const int col = 32 * h + 8 * ((i >> 1) & 3) + 2 * (src & 3) + (bit & 1);
+                        const uint2 xv = tile_quad(xbuf + (kHeld8 ? 0 : (t & 1) * TILE), r, lane), wv = tile_quad(wbuf + c * TILE, col, lane);
+                        const float2 xa = two(xv.x), xb = two(xv.y), wa = two(wv.x), wb = two(wv.y);
+                        double sum = (double)xa.x * wa.x + (double)xa.y * wa.y + (double)xb.x * wb.x + (double)xb.y * wb.y;
+#pragma unroll
+                        for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                        if (lane == src) keep = (keep & ~(1u << bit)) | (sum + (double)fbuf[c * 128 + col] > 0.0 ? 1u << bit : 0u);
+                    }
+                }
+            }
+            const bool share = has_p && ACT != LIN_RELU && can_share(p);
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+                for (int jp = 0; jp < 2; ++jp) {
+                    uint32_t dy[4];  // (row, row + 8) of column block 2 jp, then of 2 jp + 1
+                    const uint32_t at = tile + rh * 2048 + (uint32_t)(((4 * (h & 1) + 2 * jp + la_c) ^ x7) << 4);
+                    ldmatrix4(dy, at);
+                    float2 y[4], d[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        y[x] = p[rh * 8 + 4 * jp + x];
+                        d[x] = two(dy[x]);
+                    }
+                    if (ACT == LIN_RELU) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t b = keep >> (2 * (rh * 8 + 4 * jp + x));
+                            d[x] = make_float2(b & 1u ? d[x].x : 0.f, b & 2u ? d[x].y : 0.f);
+                        }
+                    } else if (has_p) {
+                        float2(&y0)[2] = *reinterpret_cast<float2(*)[2]>(&y[0]), (&y1)[2] = *reinterpret_cast<float2(*)[2]>(&y[2]);
+                        const float2 e0[2] = {d[0], d[1]}, e1[2] = {d[2], d[3]};
+                        if (share) {
+                            act_grad4<ACT, true>(y0, e0);
+                            act_grad4<ACT, true>(y1, e1);
+                        } else {
+                            act_grad4<ACT, false>(y0, e0);
+                            act_grad4<ACT, false>(y1, e1);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) d[x] = y[x];
+                    }
+#pragma unroll
+                    for (int cc = 0; cc < CHUNKS; ++cc)
+                        if (cc == c) {
+                            dbs[cc][2 * jp] = __fadd2_rn(dbs[cc][2 * jp], __fadd2_rn(d[0], d[1]));
+                            dbs[cc][2 * jp + 1] = __fadd2_rn(dbs[cc][2 * jp + 1], __fadd2_rn(d[2], d[3]));
+                        }
+                    if (has_p) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[x] = pack_bf16x2(d[x].x, d[x].y);
+                        stmatrix4(at, o);
+                    }
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dready[db]);
+            return true;
+        };
+
+        // dx of tile t: this worker's 32 rows x 32 columns.
+        auto drain_dx = [&](int t) {
+            if (!warp_wait(dxfull, (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 12, t)) return false;
+            tc_fence_after();
+            uint32_t v[32];
+            tmem_ld32(lanebase + (uint32_t)(DX_COL + 32 * h), v);
+            tmem_ld_wait_regs(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dxfree);
+            const long long r = (long long)row0(t) + 32 * q + lane;
+            const int col = 32 * h;
+            float *part = args.dx_part + (size_t)r * args.k + col;
+            if (args.dx_mode == LBW_DX_PART) {
+                if (r < args.rows)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (col + 4 * j < args.k)
+                            *reinterpret_cast<uint4 *>(part + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                return true;
+            }
+            if (args.dx_mode == LBW_DX_ADD && r < args.rows)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col + 4 * j < args.k) {
+                        const float4 f = __ldcs(reinterpret_cast<const float4 *>(part + 4 * j));
+                        v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
+                        v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
+                        v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
+                        v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
+                    }
+            if (lane == 0) tma_store_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    o[x] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * x]), __uint_as_float(v[8 * j + 2 * x + 1]));
+                *reinterpret_cast<uint4 *>(ob + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && col < args.k && row0(t) + 32 * q < args.rows) {
+                tma_store_3d(&tmDx, ob, col, row0(t) + 32 * q, 0);
+                tma_store_commit();
+            }
+            return true;
+        };
+
+        const bool has_dx = args.dx_mode != LBW_DX_NONE;
+        for (int t = 0; ok && t < my_tiles; ++t) {
+            if (kHeld8) {
+                if (has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
+                if (!(ok = convert(t))) break;
+            }
+            for (int c = 0; c < CHUNKS; ++c) {
+                if (!(ok = make_d(t * CHUNKS + c))) break;
+                if (!kHeld8 && c == 0 && has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
+            }
+        }
+        if (ok && has_dx && my_tiles > 0) ok = drain_dx(my_tiles - 1);
+        if (lane == 0) tma_store_wait_all<0>();
+        // dW, once every product is done: lane = row of the 128, 32 columns of k.
+        if (ok) ok = warp_wait(drain, 0, abort_flag, ctl, SITE_LBW | 13, 0);
+        if (ok && args.has_dw) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < CHUNKS; ++c) {
+                __syncwarp();
+                uint32_t v[32];
+                tmem_ld32(lanebase + (uint32_t)(128 * c + 32 * h), v);
+                tmem_ld_wait_regs(v);
+                const int r = c * 128 + 32 * q + lane;
+                if (r >= args.n) continue;
+                if (args.dw_out) {
+                    __nv_bfloat16 *dst = args.dw_out + (size_t)r * args.k + 32 * h;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (32 * h + 8 * j < args.k) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                o[x] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * x]), __uint_as_float(v[8 * j + 2 * x + 1]));
+                            *reinterpret_cast<uint4 *>(dst + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                } else {
+                    float *dst = args.partial + (size_t)blockIdx.x * args.part_stride + (size_t)r * args.k + 32 * h;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (32 * h + 4 * j < args.k)
+                            *reinterpret_cast<uint4 *>(dst + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+    if (!args.has_db) return;
+    // db: each worker's lanes that share columns (lane % 4) are joined, then the four row quarters. The
+    // tiles' memory is free by now.
+    float *part = reinterpret_cast<float *>(dbuf);  // [4][128 CHUNKS]
+    if (warp >= 2) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 s = dbs[c][j];
+#pragma unroll
+                for (int w = 4; w <= 16; w <<= 1) {
+                    s.x += __shfl_xor_sync(0xffffffffu, s.x, w);
+                    s.y += __shfl_xor_sync(0xffffffffu, s.y, w);
+                }
+                if (lane < 4) *reinterpret_cast<float2 *>(part + q * 128 * CHUNKS + c * 128 + 32 * h + 8 * j + 2 * lane) = s;
+            }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 128 * CHUNKS && i < args.n; i += THREADS) {
+        const float s = (part[i] + part[128 * CHUNKS + i]) + (part[256 * CHUNKS + i] + part[384 * CHUNKS + i]);
+        if (args.db_out) args.db_out[i] = __float2bfloat16_rn(s);
+        else args.sums[(size_t)blockIdx.x * args.sums_stride + i] = s;
+    }
+}
+
+namespace {
+template <int CHUNKS, bool kHeld8, int ACT>
+cudaError_t allow() {
+    return cudaFuncSetAttribute(linear_bwd_kernel<CHUNKS, kHeld8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)lb::smem(CHUNKS));
+}
+template <int CHUNKS, bool kHeld8>
+cudaError_t allow_acts() {
+    cudaError_t e;
+    if ((e = allow<CHUNKS, kHeld8, LIN_NONE>()) || (e = allow<CHUNKS, kHeld8, LIN_RELU>()) ||
+        (e = allow<CHUNKS, kHeld8, LIN_SIGMOID>()))
+        return e;
+    return allow<CHUNKS, kHeld8, LIN_SILU>();
+}
+template <int CHUNKS, bool kHeld8, int ACT>
+void go(const LinearBwdMaps &m, const LinearBwdArgs &a, int grid, cudaStream_t s) {
+    linear_bwd_kernel<CHUNKS, kHeld8, ACT><<<grid, lb::THREADS, lb::smem(CHUNKS), s>>>(m.x, m.w, m.dy, m.dx, a);
+}
+template <int CHUNKS, bool kHeld8>
+void go_act(const LinearBwdMaps &m, const LinearBwdArgs &a, int grid, cudaStream_t s) {
+    if (a.act == LIN_NONE) go<CHUNKS, kHeld8, LIN_NONE>(m, a, grid, s);
+    else if (a.act == LIN_RELU) go<CHUNKS, kHeld8, LIN_RELU>(m, a, grid, s);
+    else if (a.act == LIN_SIGMOID) go<CHUNKS, kHeld8, LIN_SIGMOID>(m, a, grid, s);
+    else go<CHUNKS, kHeld8, LIN_SILU>(m, a, grid, s);
+}
+}  // namespace
+
+cudaError_t linear_bwd_setup() {
+    cudaError_t e;
+    if ((e = allow_acts<1, false>()) || (e = allow_acts<1, true>()) || (e = allow_acts<2, false>())) return e;
+    return allow_acts<2, true>();
+}
+
+cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int grid, cudaStream_t s) {
+    if (a.n > 128) held8 ? go_act<2, true>(m, a, grid, s) : go_act<2, false>(m, a, grid, s);
+    else held8 ? go_act<1, true>(m, a, grid, s) : go_act<1, false>(m, a, grid, s);
+    return cudaGetLastError();
+}
+
+}  // namespace trimul
