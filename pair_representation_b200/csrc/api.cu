@@ -1227,7 +1227,7 @@ LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int fro
         const size_t ctas = linear_one_pass_ctas(rows);
         L.partial = take(ctas * n * k * 4);  // dW of each CTA, fp32
         L.sums = take(ctas * n * 4);         // db of each CTA
-        L.dx = take(n > 256 ? (size_t)rows * k * 4 : 0);
+        L.dx = take(n > 256 ? (size_t)ceil_div(rows, 128) * 128 * 128 * 4 : 0);  // dx between the launches, fp32
     } else {
         L.x = take(from8 ? (size_t)rows * k * 2 : 0);                   // the values of x8, bf16
         L.d = take(act != TRIMUL_ACT_NONE ? (size_t)rows * n * 2 : 0);  // D, bf16

@@ -348,7 +348,7 @@ struct LinearBwdArgs {
     const __nv_bfloat16 *bias;  // [n] or null
     const uint8_t *scales;      // x in 8 bits: [rows][k / 32], else null
     int dx_mode;
-    float *dx_part;  // [rows][k]
+    float *dx_part;  // [row_tiles][128 x 128], in the kernel's own order
     int has_dw, has_db;
     float *partial;  // [grid][part_stride]: dW [n][k] of each CTA, unless dw_out
     long long part_stride;

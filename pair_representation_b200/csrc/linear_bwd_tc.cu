@@ -69,6 +69,47 @@ __device__ __forceinline__ uint2 tile_quad(const uint8_t *tile, int r, int l) {
     return *reinterpret_cast<const uint2 *>(tile + (l >> 4) * lb::HALF + r * 128 + ((((l & 15) >> 1) ^ (r & 7)) << 4) + (l & 1) * 8);
 }
 
+// A worker's 32 x 32 block of D in place of dy, at the lane's row address `tile` (8-column chunk c0 and
+// on, row & 7 = x7); dsum gets the column sums over the lane's four rows. p as in make_d.
+template <int ACT, bool kShare>
+__device__ __forceinline__ void write_d(const float2 (&p)[16], uint32_t keep, uint32_t tile, int c0, int x7, float2 (&dsum)[4]) {
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh)
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+            uint32_t dy[4];  // (row, row + 8) of column block 2 jp, then of 2 jp + 1
+            const uint32_t at = tile + rh * 2048 + (uint32_t)(((c0 + 2 * jp) ^ x7) << 4);
+            ldmatrix4(dy, at);
+            float2 d[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) d[x] = two(dy[x]);
+            if (ACT == LIN_RELU) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t b = keep >> (2 * (rh * 8 + 4 * jp + x));
+                    d[x] = make_float2(b & 1u ? d[x].x : 0.f, b & 2u ? d[x].y : 0.f);
+                }
+            } else if (ACT != LIN_NONE) {
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                    float2 y[2] = {p[rh * 8 + 4 * jp + x], p[rh * 8 + 4 * jp + x + 1]};
+                    const float2 e[2] = {d[x], d[x + 1]};
+                    act_grad4<ACT, kShare>(y, e);
+                    d[x] = y[0];
+                    d[x + 1] = y[1];
+                }
+            }
+            dsum[2 * jp] = __fadd2_rn(dsum[2 * jp], __fadd2_rn(d[0], d[1]));
+            dsum[2 * jp + 1] = __fadd2_rn(dsum[2 * jp + 1], __fadd2_rn(d[2], d[3]));
+            if (ACT != LIN_NONE) {
+                uint32_t o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[x] = pack_bf16x2(d[x].x, d[x].y);
+                stmatrix4(at, o);
+            }
+        }
+}
+
 }  // namespace
 
 template <int CHUNKS, bool kHeld8, int ACT>
@@ -327,6 +368,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             }
             if (!warp_wait(&dfull[db], (uint32_t)(u >> 1) & 1u, abort_flag, ctl, SITE_LBW | 11, u)) return false;
             const uint32_t tile = smem_u32(dbuf + db * TILE + (h >> 1) * HALF) + la_off;
+            float2 dsum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             uint32_t keep = 0xFFFFFFFFu;  // relu: bit 2 i + e of value p[i].x or .y
             if (ACT == LIN_RELU) {
                 // The sign of a p next to 0 is taken again in 64 bits (see linear_tc.cu).
@@ -363,52 +405,16 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                     }
                 }
             }
-            const bool share = has_p && ACT != LIN_RELU && can_share(p);
+            // One test for all of the warp's values: the four blocks below then overlap, and their matrix loads
+            // and stores, which the whole warp does together, stand on one side of the branch.
+            const bool share = !has_p || ACT == LIN_RELU || __all_sync(0xffffffffu, can_share(p));
+            if (!share) write_d<ACT, false>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
+            else write_d<ACT, true>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
 #pragma unroll
-            for (int rh = 0; rh < 2; ++rh)
+            for (int cc = 0; cc < CHUNKS; ++cc)
+                if (cc == c)
 #pragma unroll
-                for (int jp = 0; jp < 2; ++jp) {
-                    uint32_t dy[4];  // (row, row + 8) of column block 2 jp, then of 2 jp + 1
-                    const uint32_t at = tile + rh * 2048 + (uint32_t)(((4 * (h & 1) + 2 * jp + la_c) ^ x7) << 4);
-                    ldmatrix4(dy, at);
-                    float2 y[4], d[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        y[x] = p[rh * 8 + 4 * jp + x];
-                        d[x] = two(dy[x]);
-                    }
-                    if (ACT == LIN_RELU) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t b = keep >> (2 * (rh * 8 + 4 * jp + x));
-                            d[x] = make_float2(b & 1u ? d[x].x : 0.f, b & 2u ? d[x].y : 0.f);
-                        }
-                    } else if (has_p) {
-                        float2(&y0)[2] = *reinterpret_cast<float2(*)[2]>(&y[0]), (&y1)[2] = *reinterpret_cast<float2(*)[2]>(&y[2]);
-                        const float2 e0[2] = {d[0], d[1]}, e1[2] = {d[2], d[3]};
-                        if (share) {
-                            act_grad4<ACT, true>(y0, e0);
-                            act_grad4<ACT, true>(y1, e1);
-                        } else {
-                            act_grad4<ACT, false>(y0, e0);
-                            act_grad4<ACT, false>(y1, e1);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) d[x] = y[x];
-                    }
-#pragma unroll
-                    for (int cc = 0; cc < CHUNKS; ++cc)
-                        if (cc == c) {
-                            dbs[cc][2 * jp] = __fadd2_rn(dbs[cc][2 * jp], __fadd2_rn(d[0], d[1]));
-                            dbs[cc][2 * jp + 1] = __fadd2_rn(dbs[cc][2 * jp + 1], __fadd2_rn(d[2], d[3]));
-                        }
-                    if (has_p) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) o[x] = pack_bf16x2(d[x].x, d[x].y);
-                        stmatrix4(at, o);
-                    }
-                }
+                    for (int j = 0; j < 4; ++j) dbs[cc][j] = __fadd2_rn(dbs[cc][j], dsum[j]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&dready[db]);
@@ -425,27 +431,25 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(dxfree);
-            const long long r = (long long)row0(t) + 32 * q + lane;
             const int col = 32 * h;
-            float *part = args.dx_part + (size_t)r * args.k + col;
+            // Between launches dx goes as the lanes hold it: 16 bytes a lane, 512 a warp and step.
+            float4 *part = reinterpret_cast<float4 *>(args.dx_part) + ((size_t)(row0(t) >> 7) * WORKERS + ew) * 256 + lane;
             if (args.dx_mode == LBW_DX_PART) {
-                if (r < args.rows)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + 4 * j < args.k)
-                            *reinterpret_cast<uint4 *>(part + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                return true;
-            }
-            if (args.dx_mode == LBW_DX_ADD && r < args.rows)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (col + 4 * j < args.k) {
-                        const float4 f = __ldcs(reinterpret_cast<const float4 *>(part + 4 * j));
-                        v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
-                        v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
-                        v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
-                        v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
-                    }
+                    part[32 * j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                               __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                return true;
+            }
+            if (args.dx_mode == LBW_DX_ADD)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = __ldcs(part + 32 * j);
+                    v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
+                    v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
+                    v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
+                    v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
+                }
             if (lane == 0) tma_store_wait_read<0>();
             __syncwarp();
 #pragma unroll

@@ -512,48 +512,57 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
 // ---------------------------------------------------------------------------
 // Sums of the split products and of the column-sum partials, rounded once to bf16.
 // dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. A block takes 32 places; its
-// eight warps each add every eighth partial (all loads of a lane independent), and
-// the eight sums are joined in shared memory in order: the result does not depend on
-// the launch. Up to 148 partials, bound by their reading.
+// sixteen warps each add every sixteenth partial (at most ten, all in flight at once), and
+// the sixteen sums are joined in shared memory in order: the result does not depend on
+// the launch. Up to 148 partials, bound by the latency of reading them.
 // ---------------------------------------------------------------------------
 namespace {
 
-__global__ void __launch_bounds__(256) linear_reduce_kernel(const LinearReduceArgs a) {
-    __shared__ float4 part[8][32];
+constexpr int kReduceWarps = 16, kReduceLoads = 10;
+
+__device__ __forceinline__ void add4(float4 &s, const float4 &v) {
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+}
+
+__global__ void __launch_bounds__(kReduceWarps * 32) linear_reduce_kernel(const LinearReduceArgs a) {
+    __shared__ float4 part[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool weight = (int)blockIdx.x < a.weight_blocks;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = zero, v[kReduceLoads];
     if (weight) {
         const long long quads = a.count >> 2;  // n k is a multiple of 64
         const long long i = (long long)blockIdx.x * 32 + lane;
-        if (i < quads) {
-            const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
-#pragma unroll 4
-            for (int k = warp; k < a.splits; k += 8) {
-                const float4 v = __ldcs(p + (size_t)k * quads);
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
+        const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
+        for (int k0 = warp; k0 < a.splits; k0 += kReduceWarps * kReduceLoads) {
+#pragma unroll
+            for (int u = 0; u < kReduceLoads; ++u) {
+                const int k = k0 + u * kReduceWarps;
+                v[u] = i < quads && k < a.splits ? __ldcs(p + (size_t)k * quads) : zero;
             }
+#pragma unroll
+            for (int u = 0; u < kReduceLoads; ++u) add4(s, v[u]);
         }
     } else {
         const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
-        if (j < a.n)
-#pragma unroll 4
-            for (int k = warp; k < a.sum_rows; k += 8) s.x += a.sums[(size_t)k * a.n + j];
+        for (int k0 = warp; k0 < a.sum_rows; k0 += kReduceWarps * kReduceLoads) {
+#pragma unroll
+            for (int u = 0; u < kReduceLoads; ++u) {
+                const int k = k0 + u * kReduceWarps;
+                v[u].x = j < a.n && k < a.sum_rows ? a.sums[(size_t)k * a.n + j] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kReduceLoads; ++u) s.x += v[u].x;
+        }
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0) return;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) {
-        const float4 v = part[k][lane];
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-    }
+    for (int k = 1; k < kReduceWarps; ++k) add4(s, part[k][lane]);
     if (weight) {
         const long long i = (long long)blockIdx.x * 32 + lane;
         if (i < a.count >> 2) reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
@@ -569,7 +578,7 @@ cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s) {
     a.weight_blocks = a.dw ? (int)((a.count / 4 + 31) / 32) : 0;
     const int grid = a.weight_blocks + (a.db ? (a.n + 31) / 32 : 0);
     if (grid == 0) return cudaSuccess;
-    linear_reduce_kernel<<<grid, 256, 0, s>>>(a);
+    linear_reduce_kernel<<<grid, kReduceWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 
