@@ -733,8 +733,10 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
                 t.zero_()
         return dx, dw, db
     code = ACTS[act]
-    ws = workspace if workspace is not None else torch.empty(
-        max(256, trimul_linear_backward_workspace_size(rows, k, n, code, held)), dtype=torch.uint8, device=weight.device)
+    ws = workspace
+    if ws is None:
+        need = trimul_linear_backward_workspace_size(rows, k, n, code, held)
+        ws = _status_workspace(weight) if need <= 256 else weight.new_empty(need, dtype=torch.uint8)
     p = LinearParams(rows, k, n, code, weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
     if held:
         trimul_linear_backward(None, Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()), dout, p, dx, dw, db,

@@ -1201,18 +1201,18 @@ LinearSplit linear_split(long long rows, int k, int n) {
     return s;
 }
 
-// The backward in one pass over the batch (linear_bwd_tc.cu) where W's slab of 256 columns fits beside
-// the tiles. Up to 512 columns of n: dx passes between the launches in fp32, 2816 bytes a row at
-// 128 -> 512 against 4864 of the three products.
+// The backward in one pass over the batch (linear_bwd_tc.cu) where W's slab of 256 rows fits beside the
+// tiles, and the slabs of two CTAs hold all of W: 1536 bytes a row at 128 -> 512 against 4864 of the
+// three products. Teams of one CTA, or of two (n > 256).
 bool linear_one_pass(int k, int n) { return k <= 128 && n <= 512; }
-int linear_one_pass_ctas(long long rows) {
-    const int tiles = ceil_div(rows, 128);
-    return tiles < kLinearCtas ? tiles : kLinearCtas;
+int linear_teams(long long rows, int n) {
+    const int tiles = ceil_div(rows, 128), most = n > 256 ? kLinearCtas / 2 : kLinearCtas;
+    return tiles < most ? tiles : most;
 }
 
 // Sections of the backward workspace (byte offsets, 256-byte aligned).
 struct LinearBwdLayout {
-    size_t x, d, partial, sums, dx, total;
+    size_t x, d, partial, sums, total;
 };
 LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int from8) {
     LinearBwdLayout L;
@@ -1224,17 +1224,18 @@ LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int fro
         return o;
     };
     if (linear_one_pass(k, n)) {
-        const size_t ctas = linear_one_pass_ctas(rows);
-        L.partial = take(ctas * n * k * 4);  // dW of each CTA, fp32
-        L.sums = take(ctas * n * 4);         // db of each CTA
-        L.dx = take(n > 256 ? (size_t)ceil_div(rows, 128) * 128 * 128 * 4 : 0);  // dx between the launches, fp32
+        const size_t teams = linear_teams(rows, n);
+        if (teams > 1) {                          // else the kernel writes dW and db themselves
+            L.partial = take(teams * n * k * 4);  // dW of each team, fp32
+            L.sums = take(teams * n * 4);         // db of each team
+        }
     } else {
         L.x = take(from8 ? (size_t)rows * k * 2 : 0);                   // the values of x8, bf16
         L.d = take(act != TRIMUL_ACT_NONE ? (size_t)rows * n * 2 : 0);  // D, bf16
         const LinearSplit s = linear_split(rows, k, n);
         L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
-        // Column sums of D: one row per part, or per row-tile group of the D product.
-        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)kLinearCtas : (size_t)s.splits;
+        // Column sums of D: one row per part, or four per row-tile group of the D product.
+        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * kLinearCtas : (size_t)s.splits;
         L.sums = take(sums * n * 4);
     }
     L.total = off;
@@ -1319,70 +1320,62 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     return cuda_rc(launch_linear_tc(m, a, mode, bn, a.col_tiles * a.groups, s), "linear_tc launch");
 }
 
-// The one-pass backward: one launch per 256 columns of n, then the sums over the CTAs.
+// The one-pass backward, then the sums over its teams.
 int run_linear_one_pass(const void *x, const trimul_act8 *x8, const void *dy, const trimul_linear_params *p, void *dx,
                         void *dw, void *db, const LinearBwdLayout &L, const KernelCtl &ctl, cudaStream_t s) {
     const int rows = (int)p->rows, k = p->in_features, n = p->out_features;
-    const int grid = linear_one_pass_ctas(rows);
+    const int teams = linear_teams(rows, n);
     uint8_t *base = static_cast<uint8_t *>(p->workspace);
-    for (int n0 = 0; n0 < n; n0 += 256) {
-        const int nn = n - n0 < 256 ? n - n0 : 256;
-        LinearBwdMaps m;
-        if (x8) {
-            const uint64_t dims[3] = {(uint64_t)k, (uint64_t)rows, 1};
-            const uint64_t strides[2] = {(uint64_t)k, (uint64_t)k * rows};
-            const uint32_t box[3] = {128, 128, 1};
-            if (int rc = encode(&m.x, 3, x8->codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_DATA_TYPE_UINT8))
-                return rc;
-        } else if (int rc = map_operand(&m.x, x, k, rows, false, 128)) {
+    LinearBwdMaps m;
+    if (x8) {
+        const uint64_t dims[3] = {(uint64_t)k, (uint64_t)rows, 1};
+        const uint64_t strides[2] = {(uint64_t)k, (uint64_t)k * rows};
+        const uint32_t box[3] = {128, 128, 1};
+        if (int rc = encode(&m.x, 3, x8->codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_DATA_TYPE_UINT8))
             return rc;
-        }
-        if (int rc = map_operand(&m.w, static_cast<const __nv_bfloat16 *>(p->weight) + (size_t)n0 * k, k, nn, false, 128))
-            return rc;
-        if (int rc = map_view(&m.dy, {static_cast<const __nv_bfloat16 *>(dy) + n0, (size_t)n, 0}, nn, rows, 1, 64, 128, 2,
-                              CU_TENSOR_MAP_DATA_TYPE_BFLOAT16))
-            return rc;
-        m.dx = m.x;  // unused without dx
-        if (dx) {
-            const uint64_t dims[3] = {(uint64_t)k, (uint64_t)rows, 1};
-            const uint64_t strides[2] = {(uint64_t)k * 2, (uint64_t)k * 2 * rows};
-            const uint32_t box[3] = {32, 32, 1};
-            if (int rc = encode(&m.dx, 3, dx, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
-        }
-        LinearBwdArgs a;
-        memset(&a, 0, sizeof a);
-        a.rows = rows;
-        a.row_tiles = ceil_div(rows, 128);
-        a.k = k;
-        a.n = nn;
-        a.act = p->act;
-        a.bias = p->bias ? static_cast<const __nv_bfloat16 *>(p->bias) + n0 : nullptr;
-        a.scales = x8 ? static_cast<const uint8_t *>(x8->scales) : nullptr;
-        a.dx_mode = !dx ? LBW_DX_NONE : n <= 256 ? LBW_DX_BF16 : n0 == 0 ? LBW_DX_PART : LBW_DX_ADD;
-        a.dx_part = reinterpret_cast<float *>(base + L.dx);
-        a.has_dw = dw != nullptr;
-        a.has_db = db != nullptr;
-        a.partial = reinterpret_cast<float *>(base + L.partial) + (size_t)n0 * k;
-        a.part_stride = (long long)n * k;
-        a.sums = reinterpret_cast<float *>(base + L.sums) + n0;
-        a.sums_stride = n;
-        if (grid == 1) {
-            a.dw_out = dw ? static_cast<__nv_bfloat16 *>(dw) + (size_t)n0 * k : nullptr;
-            a.db_out = db ? static_cast<__nv_bfloat16 *>(db) + n0 : nullptr;
-        }
-        a.clear_status = n0 == 0;
-        a.ctl = ctl;
-        if (int rc = cuda_rc(launch_linear_bwd(m, a, x8 != nullptr, grid, s), "linear_bwd launch")) return rc;
+    } else if (int rc = map_operand(&m.x, x, k, rows, false, 128)) {
+        return rc;
     }
-    if (grid == 1) return TRIMUL_OK;
+    if (int rc = map_operand(&m.w, p->weight, k, n, false, 128)) return rc;
+    if (int rc = map_operand(&m.dy, dy, n, rows, false, 128)) return rc;
+    m.dx = m.x;  // unused without dx
+    if (dx) {
+        const uint64_t dims[3] = {(uint64_t)k, (uint64_t)rows, 1};
+        const uint64_t strides[2] = {(uint64_t)k * 2, (uint64_t)k * 2 * rows};
+        const uint32_t box[3] = {32, 32, 1};
+        if (int rc = encode(&m.dx, 3, dx, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
+    }
+    LinearBwdArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.row_tiles = ceil_div(rows, 128);
+    a.k = k;
+    a.n = n;
+    a.act = p->act;
+    a.bias = static_cast<const __nv_bfloat16 *>(p->bias);
+    a.scales = x8 ? static_cast<const uint8_t *>(x8->scales) : nullptr;
+    a.has_dx = dx != nullptr;
+    a.has_dw = dw != nullptr;
+    a.has_db = db != nullptr;
+    if (teams == 1) {
+        a.dw_out = static_cast<__nv_bfloat16 *>(dw);
+        a.db_out = static_cast<__nv_bfloat16 *>(db);
+    } else {
+        a.partial = reinterpret_cast<float *>(base + L.partial);
+        a.sums = reinterpret_cast<float *>(base + L.sums);
+    }
+    a.clear_status = 1;
+    a.ctl = ctl;
+    if (int rc = cuda_rc(launch_linear_bwd(m, a, x8 != nullptr, teams, s), "linear_bwd launch")) return rc;
+    if (teams == 1) return TRIMUL_OK;
     LinearReduceArgs r;
     memset(&r, 0, sizeof r);
-    r.partial = reinterpret_cast<const float *>(base + L.partial);
+    r.partial = a.partial;
     r.dw = static_cast<__nv_bfloat16 *>(dw);
     r.count = (long long)n * k;
-    r.splits = r.sum_rows = grid;
-    r.sums = reinterpret_cast<const float *>(base + L.sums);
+    r.splits = r.sum_rows = teams;
+    r.sums = a.sums;
     r.db = static_cast<__nv_bfloat16 *>(db);
     r.n = n;
     return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");

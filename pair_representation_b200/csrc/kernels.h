@@ -333,29 +333,18 @@ cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s);
 
 // ---- the backward in one pass, in_features <= 128 (linear_bwd_tc.cu) ---------------
 
-enum LinearBwdDx {
-    LBW_DX_NONE = 0,  // not wanted
-    LBW_DX_BF16 = 1,  // written
-    LBW_DX_PART = 2,  // written to dx_part in fp32
-    LBW_DX_ADD = 3,   // added to dx_part and written
-};
-
 struct LinearBwdArgs {
     long long rows;
     int row_tiles;  // of 128 rows
-    int k, n;       // k <= 128; n <= 256: columns of dy that this launch takes
+    int k, n;       // k <= 128, n <= 512
     int act;
     const __nv_bfloat16 *bias;  // [n] or null
     const uint8_t *scales;      // x in 8 bits: [rows][k / 32], else null
-    int dx_mode;
-    float *dx_part;  // [row_tiles][128 x 128], in the kernel's own order
-    int has_dw, has_db;
-    float *partial;  // [grid][part_stride]: dW [n][k] of each CTA, unless dw_out
-    long long part_stride;
-    __nv_bfloat16 *dw_out;  // [n][k], one CTA
-    float *sums;            // [grid][sums_stride]: db of each CTA, unless db_out
-    int sums_stride;
-    __nv_bfloat16 *db_out;  // [n], one CTA
+    int has_dx, has_dw, has_db;
+    float *partial;         // [teams][n][k]: dW of each team of CTAs, unless dw_out
+    float *sums;            // [teams][n]: db of each team, unless db_out
+    __nv_bfloat16 *dw_out;  // [n][k], one team
+    __nv_bfloat16 *db_out;  // [n], one team
     int clear_status;
     KernelCtl ctl;
 };
@@ -367,7 +356,8 @@ struct LinearBwdMaps {
 };
 
 cudaError_t linear_bwd_setup();
-cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int grid, cudaStream_t s);
+// teams: CTAs, or pairs of CTAs where n > 256.
+cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int teams, cudaStream_t s);
 
 // ---- activations in 8 bits (act8.cu); values: a multiple of 32 -------------------
 

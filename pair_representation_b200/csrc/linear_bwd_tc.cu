@@ -14,7 +14,8 @@
 //   * dx leaves tensor memory once per tile; dW stays there as a running sum over all the CTA's
 //     tiles (128 or 256 columns) and is written once, in fp32, for linear_reduce_kernel to add up
 //     the CTAs' parts in order; db likewise, summed from D before its rounding.
-// n over 256: one call per 256 columns of n, dx passing between them in fp32.
+// n over 256 (kPair): two CTAs of a cluster take the same rows and 256 columns of n each, and send
+// each other half of their parts of dx through distributed shared memory.
 // kHeld8: x comes as E4M3 codes and E8M0 scales; the workers turn each tile into bf16 as it
 // arrives, so the 8-bit form is all that is read.
 //
@@ -40,7 +41,7 @@ constexpr int WORKERS = 16;
 constexpr int THREADS = (2 + WORKERS) * 32;
 constexpr int CODES = 128 * 128;          // a tile's codes
 constexpr int OUT = 32 * 64;              // a worker's block of dx: 32 rows x 32 columns
-constexpr int BAR_BYTES = 256;
+constexpr int BAR_BYTES = 384;
 __host__ __device__ constexpr size_t smem(int chunks) {
     // W, x (two tiles; kHeld8: one, and two of codes), D (two), dx blocks, bias and db sums
     return 1024 + (size_t)chunks * TILE + 2 * TILE + 2 * TILE + WORKERS * OUT + 1024 + BAR_BYTES;
@@ -63,6 +64,10 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4])
                  : "memory");
 }
 __device__ __forceinline__ float2 two(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+__device__ __forceinline__ void st_remote_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
 // Four bf16 at column 4 l of row r of a 128 x 128 tile.
 __device__ __forceinline__ uint2 tile_quad(const uint8_t *tile, int r, int l) {
@@ -112,7 +117,7 @@ __device__ __forceinline__ void write_d(const float2 (&p)[16], uint32_t keep, ui
 
 }  // namespace
 
-template <int CHUNKS, bool kHeld8, int ACT>
+template <int CHUNKS, bool kPair, bool kHeld8, int ACT>
 __global__ void __launch_bounds__(lb::THREADS, 1)
     linear_bwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmDx,
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     uint8_t *xbuf = wbuf + CHUNKS * TILE;               // kHeld8: one tile, else two
     uint8_t *codes = xbuf + TILE;                       // kHeld8: [2]
     uint8_t *dbuf = xbuf + 2 * TILE;                    // [2] dy, then D
-    uint8_t *obuf = dbuf + 2 * TILE;                    // [WORKERS]
+    uint8_t *obuf = dbuf + 2 * TILE;                    // [WORKERS] 2 KB; kPair: [8] 4 KB
     float *fbuf = reinterpret_cast<float *>(obuf + WORKERS * OUT);  // bias [256]; at the end db sums
     uint64_t *bars = reinterpret_cast<uint64_t *>(fbuf + 256);
     uint64_t *wfull = bars;            // W landed
@@ -142,15 +147,21 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     uint64_t *dxfull = bars + 18;      // dx of a tile complete
     uint64_t *dxfree = bars + 19;      // dx read (WORKERS arrivals)
     uint64_t *drain = bars + 20;       // every product is done
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 21);
+    uint64_t *rfull = bars + 21;       // kPair: [8] the peer's part of a block of dx is here
+    uint64_t *sfree = bars + 29;       // kPair: [8] the peer has room for the next part
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 37);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KernelCtl &ctl = args.ctl;
-    const int my_tiles = ((int)args.row_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    // kPair: the two CTAs of a cluster take the same rows, each 256 columns of n from n_first.
+    const uint32_t rank = kPair ? cluster_rank() : 0u;
+    const int team = kPair ? (int)blockIdx.x >> 1 : (int)blockIdx.x, teams = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
+    const int n_first = 256 * (int)rank, n_mine = min(args.n - n_first, 128 * CHUNKS);
+    const int my_tiles = (args.row_tiles - team + teams - 1) / teams;
     const int units = my_tiles * CHUNKS;
     constexpr bool has_p = ACT != LIN_NONE;
-    auto row0 = [&](int t) { return ((int)blockIdx.x + t * (int)gridDim.x) * 128; };
+    auto row0 = [&](int t) { return (team + t * teams) * 128; };
 
     if (threadIdx.x == 0) {
         mbar_init(wfull, 1);
@@ -168,21 +179,27 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             mbar_init(&pfull[i], 1);
             mbar_init(&pfree[i], WORKERS);
         }
+        if (kPair)
+            for (int i = 0; i < 8; ++i) {
+                mbar_init(&rfull[i], 1);
+                mbar_init(&sfree[i], 1);
+            }
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmDy);
-        if (args.dx_mode == LBW_DX_BF16 || args.dx_mode == LBW_DX_ADD) tma_prefetch_desc(&tmDx);
+        if (args.has_dx) tma_prefetch_desc(&tmDx);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
     for (int i = threadIdx.x; i < 128 * CHUNKS; i += THREADS)
-        fbuf[i] = (args.bias && i < args.n) ? __bfloat162float(args.bias[i]) : 0.f;
+        fbuf[i] = (args.bias && i < n_mine) ? __bfloat162float(args.bias[n_first + i]) : 0.f;
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // the peer's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
@@ -203,7 +220,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             int xs = 0, ds = 0;  // tiles of x and units of dy asked for
             mbar_arrive_expect_tx(wfull, CHUNKS * TILE);
             for (int c = 0; c < CHUNKS; ++c)
-                for (int kb = 0; kb < 2; ++kb) tma_load_3d(wbuf + c * TILE + kb * HALF, &tmW, wfull, kb * 64, c * 128, 0);
+                for (int kb = 0; kb < 2; ++kb) tma_load_3d(wbuf + c * TILE + kb * HALF, &tmW, wfull, kb * 64, n_first + c * 128, 0);
             for (int u = 0; ok && u < units; ++u) {
                 const int t = u / CHUNKS, c = u - t * CHUNKS;
                 if (c == 0) {
@@ -224,7 +241,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 if (u >= 2 && !(ok = wait_bounded(&dfree[db], (uint32_t)((u >> 1) - 1) & 1u, abort_flag, ctl, SITE_LBW | 2, u))) break;
                 mbar_arrive_expect_tx(&dfull[db], TILE);
                 for (int nb = 0; nb < 2; ++nb)
-                    tma_load_3d(dbuf + db * TILE + nb * HALF, &tmDy, &dfull[db], c * 128 + nb * 64, row0(t), 0);
+                    tma_load_3d(dbuf + db * TILE + nb * HALF, &tmDy, &dfull[db], n_first + c * 128 + nb * 64, row0(t), 0);
                 ++ds;
             }
             // No copy may be in flight when the CTA leaves.
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                         mma_bf16(tmem + 128 * c, sdesc_sw128(dt + j * 2048, HALF, 1024), sdesc_sw128(xtile(t) + j * 2048, HALF, 1024),
                                  i_dw, (t | j) ? 1u : 0u);
                 }
-                if (args.dx_mode != LBW_DX_NONE) {
+                if (args.has_dx) {
                     if (c == 0 && t > 0) {
                         if (!(ok = wait_bounded(dxfree, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 7, t))) break;
                         tc_fence_after();
@@ -298,7 +315,22 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         // ---------------- workers ----------------
         const uint32_t la_off = (uint32_t)((32 * q + (lane & 7) + ((lane >> 3) & 1) * 8) * 128);  // row of an ldmatrix address
         const int la_c = lane >> 4, x7 = lane & 7;
-        uint8_t *ob = obuf + ew * OUT;
+        // kPair: dx is the sum of both CTAs' products. Columns 0-63 are finished by rank 0, 64-127 by rank 1: a
+        // worker of the other half sends its 32 x 32 block, in the order its lanes hold it, to the worker with
+        // the same rows and columns of the peer, which adds its own.
+        const bool home = !kPair || (h >> 1) == (int)rank;
+        const int pslot = 2 * q + (h & 1);
+        uint8_t *ob = kPair ? obuf + pslot * 4096 : obuf + ew * OUT;
+        bool owes_room = false;  // the block's buffer is still to be given back to the sender
+        auto give_room = [&]() {
+            if (kPair && owes_room) {
+                if (lane == 0) {
+                    tma_store_wait_read<0>();
+                    mbar_arrive_remote(map_to_rank(&sfree[pslot], rank ^ 1u));
+                }
+                owes_room = false;
+            }
+        };
         // kHeld8: thread (row, 32-column block) of the conversion
         const int crow = ew * 8 + (lane >> 2), cblk = lane & 3, kblk = args.k >> 5;
 
@@ -342,6 +374,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         // D of unit u in place of dy; db of its columns.
         auto make_d = [&](int u) {
             const int t = u / CHUNKS, c = u - t * CHUNKS, a = u % PRE, db = u & 1;
+            give_room();
             float2 p[16];  // [16-row half][8-column block][row, row + 8]
             if (has_p) {
                 if (!warp_wait(&pfull[a], (uint32_t)(u / PRE) & 1u, abort_flag, ctl, SITE_LBW | 10, u)) return false;
@@ -432,24 +465,31 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(dxfree);
             const int col = 32 * h;
-            // Between launches dx goes as the lanes hold it: 16 bytes a lane, 512 a warp and step.
-            float4 *part = reinterpret_cast<float4 *>(args.dx_part) + ((size_t)(row0(t) >> 7) * WORKERS + ew) * 256 + lane;
-            if (args.dx_mode == LBW_DX_PART) {
+            if (kPair && !home) {
+                if (t > 0 && !warp_wait(&sfree[pslot], (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
+                fence_acq_rel_cluster();
+                const uint32_t dst = map_to_rank(ob, rank ^ 1u) + lane * 16;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    part[32 * j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                               __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                for (int j = 0; j < 8; ++j) st_remote_v4(dst + j * 512, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                fence_acq_rel_cluster();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(map_to_rank(&rfull[pslot], rank ^ 1u));
                 return true;
             }
-            if (args.dx_mode == LBW_DX_ADD)
+            if (kPair) {
+                if (!warp_wait(&rfull[pslot], (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
+                fence_acq_rel_cluster();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float4 f = __ldcs(part + 32 * j);
+                    const float4 f = *reinterpret_cast<const float4 *>(ob + j * 512 + lane * 16);
                     v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
                     v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
                     v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
                     v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
                 }
+                __syncwarp();  // the block has been read: it now stages the result
+                owes_room = true;
+            }
             if (lane == 0) tma_store_wait_read<0>();
             __syncwarp();
 #pragma unroll
@@ -469,7 +509,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             return true;
         };
 
-        const bool has_dx = args.dx_mode != LBW_DX_NONE;
+        const bool has_dx = args.has_dx != 0;
         for (int t = 0; ok && t < my_tiles; ++t) {
             if (kHeld8) {
                 if (has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
@@ -492,8 +532,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 uint32_t v[32];
                 tmem_ld32(lanebase + (uint32_t)(128 * c + 32 * h), v);
                 tmem_ld_wait_regs(v);
-                const int r = c * 128 + 32 * q + lane;
-                if (r >= args.n) continue;
+                const int rc = c * 128 + 32 * q + lane, r = n_first + rc;
+                if (rc >= n_mine) continue;
                 if (args.dw_out) {
                     __nv_bfloat16 *dst = args.dw_out + (size_t)r * args.k + 32 * h;
 #pragma unroll
@@ -506,7 +546,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                             *reinterpret_cast<uint4 *>(dst + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                 } else {
-                    float *dst = args.partial + (size_t)blockIdx.x * args.part_stride + (size_t)r * args.k + 32 * h;
+                    float *dst = args.partial + ((size_t)team * args.n + r) * args.k + 32 * h;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (32 * h + 4 * j < args.k)
@@ -518,6 +558,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // no CTA leaves while its peer may still write to it
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
     if (!args.has_db) return;
@@ -539,50 +580,63 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 128 * CHUNKS && i < args.n; i += THREADS) {
+    for (int i = threadIdx.x; i < n_mine; i += THREADS) {
         const float s = (part[i] + part[128 * CHUNKS + i]) + (part[256 * CHUNKS + i] + part[384 * CHUNKS + i]);
-        if (args.db_out) args.db_out[i] = __float2bfloat16_rn(s);
-        else args.sums[(size_t)blockIdx.x * args.sums_stride + i] = s;
+        if (args.db_out) args.db_out[n_first + i] = __float2bfloat16_rn(s);
+        else args.sums[(size_t)team * args.n + n_first + i] = s;
     }
 }
 
 namespace {
-template <int CHUNKS, bool kHeld8, int ACT>
+template <int CHUNKS, bool kPair, bool kHeld8, int ACT>
 cudaError_t allow() {
-    return cudaFuncSetAttribute(linear_bwd_kernel<CHUNKS, kHeld8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(linear_bwd_kernel<CHUNKS, kPair, kHeld8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)lb::smem(CHUNKS));
 }
-template <int CHUNKS, bool kHeld8>
+template <int CHUNKS, bool kPair, bool kHeld8>
 cudaError_t allow_acts() {
     cudaError_t e;
-    if ((e = allow<CHUNKS, kHeld8, LIN_NONE>()) || (e = allow<CHUNKS, kHeld8, LIN_RELU>()) ||
-        (e = allow<CHUNKS, kHeld8, LIN_SIGMOID>()))
+    if ((e = allow<CHUNKS, kPair, kHeld8, LIN_NONE>()) || (e = allow<CHUNKS, kPair, kHeld8, LIN_RELU>()) ||
+        (e = allow<CHUNKS, kPair, kHeld8, LIN_SIGMOID>()))
         return e;
-    return allow<CHUNKS, kHeld8, LIN_SILU>();
+    return allow<CHUNKS, kPair, kHeld8, LIN_SILU>();
 }
-template <int CHUNKS, bool kHeld8, int ACT>
-void go(const LinearBwdMaps &m, const LinearBwdArgs &a, int grid, cudaStream_t s) {
-    linear_bwd_kernel<CHUNKS, kHeld8, ACT><<<grid, lb::THREADS, lb::smem(CHUNKS), s>>>(m.x, m.w, m.dy, m.dx, a);
+template <int CHUNKS, bool kPair, bool kHeld8, int ACT>
+cudaError_t go(const LinearBwdMaps &m, const LinearBwdArgs &a, int teams, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(kPair ? 2 * teams : teams));
+    cfg.blockDim = dim3(lb::THREADS);
+    cfg.dynamicSmemBytes = lb::smem(CHUNKS);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = kPair ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_bwd_kernel<CHUNKS, kPair, kHeld8, ACT>, m.x, m.w, m.dy, m.dx, a);
 }
-template <int CHUNKS, bool kHeld8>
-void go_act(const LinearBwdMaps &m, const LinearBwdArgs &a, int grid, cudaStream_t s) {
-    if (a.act == LIN_NONE) go<CHUNKS, kHeld8, LIN_NONE>(m, a, grid, s);
-    else if (a.act == LIN_RELU) go<CHUNKS, kHeld8, LIN_RELU>(m, a, grid, s);
-    else if (a.act == LIN_SIGMOID) go<CHUNKS, kHeld8, LIN_SIGMOID>(m, a, grid, s);
-    else go<CHUNKS, kHeld8, LIN_SILU>(m, a, grid, s);
+template <int CHUNKS, bool kPair, bool kHeld8>
+cudaError_t go_act(const LinearBwdMaps &m, const LinearBwdArgs &a, int teams, cudaStream_t s) {
+    if (a.act == LIN_NONE) return go<CHUNKS, kPair, kHeld8, LIN_NONE>(m, a, teams, s);
+    if (a.act == LIN_RELU) return go<CHUNKS, kPair, kHeld8, LIN_RELU>(m, a, teams, s);
+    if (a.act == LIN_SIGMOID) return go<CHUNKS, kPair, kHeld8, LIN_SIGMOID>(m, a, teams, s);
+    return go<CHUNKS, kPair, kHeld8, LIN_SILU>(m, a, teams, s);
 }
 }  // namespace
 
 cudaError_t linear_bwd_setup() {
     cudaError_t e;
-    if ((e = allow_acts<1, false>()) || (e = allow_acts<1, true>()) || (e = allow_acts<2, false>())) return e;
-    return allow_acts<2, true>();
+    if ((e = allow_acts<1, false, false>()) || (e = allow_acts<1, false, true>()) || (e = allow_acts<2, false, false>()) ||
+        (e = allow_acts<2, false, true>()) || (e = allow_acts<2, true, false>()))
+        return e;
+    return allow_acts<2, true, true>();
 }
 
-cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int grid, cudaStream_t s) {
-    if (a.n > 128) held8 ? go_act<2, true>(m, a, grid, s) : go_act<2, false>(m, a, grid, s);
-    else held8 ? go_act<1, true>(m, a, grid, s) : go_act<1, false>(m, a, grid, s);
-    return cudaGetLastError();
+cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bool held8, int teams, cudaStream_t s) {
+    if (a.n > 256) return held8 ? go_act<2, true, true>(m, a, teams, s) : go_act<2, true, false>(m, a, teams, s);
+    if (a.n > 128) return held8 ? go_act<2, false, true>(m, a, teams, s) : go_act<2, false, false>(m, a, teams, s);
+    return held8 ? go_act<1, false, true>(m, a, teams, s) : go_act<1, false, false>(m, a, teams, s);
 }
 
 }  // namespace trimul

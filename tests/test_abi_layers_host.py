@@ -47,7 +47,7 @@ def test_linear_sizes(L):
     for act in range(4):
         for rows in (1, 63, 64, 65, 5000):
             a = tm.trimul_linear_backward_workspace_size(rows, 128, 64, act)
-            assert a > 256
+            assert a >= 256  # the status word, and nothing else where one team of CTAs does it all
             assert tm.trimul_linear_backward_workspace_size(rows, 128, 64, act, True) >= a
     for bad in ((0, 128, 64, 0), (-1, 128, 64, 0), (1 << 31, 128, 64, 0), (10, 0, 64, 0), (10, 12, 64, 0),
                 (10, 128, 20, 0), (10, 128, 64, 4), (10, 128, 64, -1), (10, 16392, 64, 0)):

@@ -145,8 +145,10 @@ def test_backward_from_8_bits(rows, k, n, act):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("held", [True, False])
-def test_backward_many_rows(act, held):
-    check_backward(148 * 128 + 77, 128, 128, act, held=held)
+@pytest.mark.parametrize("k,n", [(128, 128), (96, 200), (64, 264), (128, 392), (128, 512), (160, 72)])
+def test_backward_many_rows(k, n, act, held):
+    """More row tiles than teams of CTAs, for each way the backward is done."""
+    check_backward(148 * 128 + 77, k, n, act, held=held)
 
 
 @pytest.mark.parametrize("act", ["none", "silu"])
@@ -200,8 +202,11 @@ def test_residual_in_place():
     assert got is r and torch.equal(got, ref)
 
 
-def test_nothing_around_the_outputs_is_written():
-    rows, k, n = 77, 72, 136
+@pytest.mark.parametrize("rows,k,n", [(77, 72, 136), (19000, 96, 200), (19000, 128, 392), (77, 160, 72), (19000, 160, 72),
+                                      (19000, 72, 520)])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_nothing_around_the_outputs_is_written(rows, k, n, act):
+    """Outputs and workspace inside larger buffers, the workspace exactly as large as it has to be."""
     x, w, b, dy = (dev(t) for t in draw(rows, k, n, 6))
 
     def frame(count):
@@ -209,17 +214,17 @@ def test_nothing_around_the_outputs_is_written():
         return t, t[128:128 + count]
 
     (fy, y), (fx, dx), (fw, dw), (fb, db) = (frame(c) for c in (rows * n, rows * k, n * k, n))
-    need = tm.trimul_linear_backward_workspace_size(rows, k, n, 3)
-    fws = torch.full((need + 256,), 9, dtype=torch.uint8, device=DEV)
-    p = tm.LinearParams(rows, k, n, 3, w.data_ptr(), b.data_ptr(), fws.data_ptr(), need, 0)
+    need = tm.trimul_linear_backward_workspace_size(rows, k, n, tm.ACTS[act])
+    fws = torch.full((need + (1 << 20),), 9, dtype=torch.uint8, device=DEV)
+    p = tm.LinearParams(rows, k, n, tm.ACTS[act], w.data_ptr(), b.data_ptr(), fws.data_ptr(), need, 0)
     tm.trimul_linear_forward(x, None, p, y)
     tm.trimul_linear_backward(x, None, dy, p, dx, dw, db)
     torch.cuda.synchronize()
     for f, v in ((fy, y), (fx, dx), (fw, dw), (fb, db)):
         assert (f[:128] == 7).all() and (f[128 + v.numel():] == 7).all()
     assert (fws[need:] == 9).all()
-    assert torch.equal(y.view(rows, n), tm.linear(x, w, bias=b, act="silu"))
-    for v, t in zip((dx, dw, db), tm.linear_backward(x, w, dy, bias=b, act="silu")):
+    assert torch.equal(y.view(rows, n), tm.linear(x, w, bias=b, act=act))
+    for v, t in zip((dx, dw, db), tm.linear_backward(x, w, dy, bias=b, act=act)):
         assert torch.equal(v.view(t.shape), t)
 
 
