@@ -65,8 +65,14 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4])
 }
 __device__ __forceinline__ float2 two(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
-__device__ __forceinline__ void st_remote_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+// 16 bytes into a CTA of the cluster, counted on a barrier there when they land: the sender need not
+// wait for its stores (a fence for plain remote ones took 5500 cycles a tile).
+__device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t cluster_bar, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(cluster_addr),
+        "r"(cluster_bar), "r"(a), "r"(b), "r"(c), "r"(d)
+        : "memory");
 }
 
 // Four bf16 at column 4 l of row r of a 128 x 128 tile.
@@ -149,7 +155,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     uint64_t *drain = bars + 20;       // every product is done
     uint64_t *rfull = bars + 21;       // kPair: [8] the peer's part of a block of dx is here
     uint64_t *sfree = bars + 29;       // kPair: [8] the peer has room for the next part
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 37);
+    volatile uint32_t *sent = reinterpret_cast<volatile uint32_t *>(bars + 37);  // kPair: [8] parts the peer has sent
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 41);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         }
         if (kPair)
             for (int i = 0; i < 8; ++i) {
+                sent[i] = 0;
                 mbar_init(&rfull[i], 1);
                 mbar_init(&sfree[i], 1);
             }
@@ -213,6 +221,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     const int ew = warp - 2, q = warp & 3, h = ew >> 2;  // worker: rows 32 q .., columns 32 h .. of a tile
     const uint32_t lanebase = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = true;
+    int my_parts = 0;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -322,6 +331,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         const int pslot = 2 * q + (h & 1);
         uint8_t *ob = kPair ? obuf + pslot * 4096 : obuf + ew * OUT;
         bool owes_room = false;  // the block's buffer is still to be given back to the sender
+        int parts = 0;           // parts of dx sent, or waited for
         auto give_room = [&]() {
             if (kPair && owes_room) {
                 if (lane == 0) {
@@ -466,19 +476,18 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             if (lane == 0) mbar_arrive(dxfree);
             const int col = 32 * h;
             if (kPair && !home) {
-                if (t > 0 && !warp_wait(&sfree[pslot], (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
-                fence_acq_rel_cluster();
+                if (t > 0 && !warp_wait_cluster(&sfree[pslot], (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
                 const uint32_t dst = map_to_rank(ob, rank ^ 1u) + lane * 16;
+                const uint32_t bar = map_to_rank(&rfull[pslot], rank ^ 1u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) st_remote_v4(dst + j * 512, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                fence_acq_rel_cluster();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(map_to_rank(&rfull[pslot], rank ^ 1u));
+                for (int j = 0; j < 8; ++j) st_async_v4(dst + j * 512, bar, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                ++parts;
                 return true;
             }
             if (kPair) {
-                if (!warp_wait(&rfull[pslot], (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
-                fence_acq_rel_cluster();
+                if (lane == 0) mbar_arrive_expect_tx(&rfull[pslot], 4096);
+                ++parts;
+                if (!warp_wait_cluster(&rfull[pslot], (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 15, t)) return false;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float4 f = *reinterpret_cast<const float4 *>(ob + j * 512 + lane * 16);
@@ -522,6 +531,11 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         }
         if (ok && has_dx && my_tiles > 0) ok = drain_dx(my_tiles - 1);
         if (lane == 0) tma_store_wait_all<0>();
+        if (kPair) {
+            // How many parts were sent, so that after a timeout the receiver can let the last one land.
+            if (!home && lane == 0) st_remote_u32(map_to_rank((const void *)&sent[pslot], rank ^ 1u), (uint32_t)parts);
+            my_parts = parts;
+        }
         // dW, once every product is done: lane = row of the 128, 32 columns of k.
         if (ok) ok = warp_wait(drain, 0, abort_flag, ctl, SITE_LBW | 13, 0);
         if (ok && args.has_dw) {
@@ -558,7 +572,17 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (kPair) cluster_sync();  // no CTA leaves while its peer may still write to it
+    if (kPair) {
+        cluster_sync();  // the counts of parts sent are here
+        if (warp >= 2 && (h >> 1) == (int)rank && lane == 0) {
+            // At most one part can be under way: the sender waits for room. A complete pass has taken all.
+            const int slot = 2 * q + (h & 1), n_sent = (int)sent[slot];
+            if (n_sent > my_parts) mbar_arrive_expect_tx(&rfull[slot], 4096);
+            if (n_sent > 0) wait_drain(&rfull[slot], (uint32_t)(n_sent - 1) & 1u, ctl.timeout_ns);
+        }
+        __syncthreads();
+        cluster_sync();
+    }
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
     if (!args.has_db) return;
