@@ -42,11 +42,13 @@ constexpr int THREADS = (2 + WORKERS) * 32;
 constexpr int CODES = 128 * 128;          // a tile's codes
 constexpr int OUT = 32 * 64;              // a worker's block of dx: 32 rows x 32 columns
 constexpr int BAR_BYTES = 384;
-__host__ __device__ constexpr size_t smem(int chunks) {
-    // W, x (two tiles; kHeld8: one, and two of codes), D (two), dx blocks, bias and db sums
-    return 1024 + (size_t)chunks * TILE + 2 * TILE + 2 * TILE + WORKERS * OUT + 1024 + BAR_BYTES;
-}
-static_assert(smem(2) <= 232448, "shared memory budget");
+// Four 32 KB tiles for W's slab and x: what W leaves is x's (with three tiles of x the next p need not
+// wait for a load behind the last dW: 40 -> 37.5 us at 147456 x 128 -> 128). kHeld8: one tile of
+// x in bf16, and the rest of x's share as 16 KB tiles of codes. Two tiles of dy, and 32 KB of dx blocks.
+__host__ __device__ constexpr int xbufs(int chunks) { return 4 - chunks; }
+__host__ __device__ constexpr int cbufs(int chunks) { return 2 * (3 - chunks); }
+constexpr size_t SMEM = 1024 + 7 * (size_t)TILE + 1024 + BAR_BYTES;
+static_assert(SMEM <= 232448, "shared memory budget");
 constexpr int TMEM_COLS = 512, DX_COL = 384;
 }  // namespace lb
 
@@ -131,32 +133,34 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     using namespace lb;
     constexpr int PRE = CHUNKS == 1 ? 2 : 1;     // accumulators of p
     constexpr int PRE_COL = 128 * CHUNKS;
+    constexpr int XB = kHeld8 ? cbufs(CHUNKS) : xbufs(CHUNKS);  // tiles of x (codes) in flight
+    static_assert(XB <= 4, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *wbuf = smem;                               // [CHUNKS] 128 rows of W
-    uint8_t *xbuf = wbuf + CHUNKS * TILE;               // kHeld8: one tile, else two
-    uint8_t *codes = xbuf + TILE;                       // kHeld8: [2]
-    uint8_t *dbuf = xbuf + 2 * TILE;                    // [2] dy, then D
+    uint8_t *xbuf = wbuf + CHUNKS * TILE;               // [XB]; kHeld8: one tile
+    uint8_t *codes = xbuf + TILE;                       // kHeld8: [XB]
+    uint8_t *dbuf = xbuf + xbufs(CHUNKS) * TILE;        // [2] dy, then D
     uint8_t *obuf = dbuf + 2 * TILE;                    // [WORKERS] 2 KB; kPair: [8] 4 KB
     float *fbuf = reinterpret_cast<float *>(obuf + WORKERS * OUT);  // bias [256]; at the end db sums
     uint64_t *bars = reinterpret_cast<uint64_t *>(fbuf + 256);
     uint64_t *wfull = bars;            // W landed
-    uint64_t *xfull = bars + 1;        // [2] x (kHeld8: codes) landed
-    uint64_t *xready = bars + 3;       // kHeld8: x turned into bf16 (WORKERS arrivals)
-    uint64_t *cfree = bars + 4;        // kHeld8: [2] codes read (WORKERS arrivals)
-    uint64_t *xfree = bars + 6;        // [2] products reading x are done
-    uint64_t *dfull = bars + 8;        // [2] dy landed
-    uint64_t *dready = bars + 10;      // [2] D written (WORKERS arrivals)
-    uint64_t *dfree = bars + 12;       // [2] products reading D are done
-    uint64_t *pfull = bars + 14;       // [2] p complete
-    uint64_t *pfree = bars + 16;       // [2] p read (WORKERS arrivals)
-    uint64_t *dxfull = bars + 18;      // dx of a tile complete
-    uint64_t *dxfree = bars + 19;      // dx read (WORKERS arrivals)
-    uint64_t *drain = bars + 20;       // every product is done
-    uint64_t *rfull = bars + 21;       // kPair: [8] the peer's part of a block of dx is here
-    uint64_t *sfree = bars + 29;       // kPair: [8] the peer has room for the next part
-    volatile uint32_t *sent = reinterpret_cast<volatile uint32_t *>(bars + 37);  // kPair: [8] parts the peer has sent
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 41);
+    uint64_t *xfull = bars + 1;        // [XB] x (kHeld8: codes) landed
+    uint64_t *xfree = bars + 5;        // [XB] products reading x are done (kHeld8: codes read, WORKERS arrivals)
+    uint64_t *xready = bars + 9;       // kHeld8: x turned into bf16 (WORKERS arrivals)
+    uint64_t *xdone = bars + 10;       // kHeld8: products reading x are done
+    uint64_t *dfull = bars + 11;       // [2] dy landed
+    uint64_t *dready = bars + 13;      // [2] D written (WORKERS arrivals)
+    uint64_t *dfree = bars + 15;       // [2] products reading D are done
+    uint64_t *pfull = bars + 17;       // [2] p complete
+    uint64_t *pfree = bars + 19;       // [2] p read (WORKERS arrivals)
+    uint64_t *dxfull = bars + 21;      // dx of a tile complete
+    uint64_t *dxfree = bars + 22;      // dx read (WORKERS arrivals)
+    uint64_t *drain = bars + 23;       // every product is done
+    uint64_t *rfull = bars + 24;       // kPair: [8] the peer's part of a block of dx is here
+    uint64_t *sfree = bars + 32;       // kPair: [8] the peer has room for the next part
+    volatile uint32_t *sent = reinterpret_cast<volatile uint32_t *>(bars + 40);  // kPair: [8] parts the peer has sent
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 44);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -173,13 +177,15 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(wfull, 1);
         mbar_init(xready, WORKERS);
+        mbar_init(xdone, 1);
+        for (int i = 0; i < XB; ++i) {
+            mbar_init(&xfull[i], 1);
+            mbar_init(&xfree[i], kHeld8 ? WORKERS : 1);
+        }
         mbar_init(dxfull, 1);
         mbar_init(dxfree, WORKERS);
         mbar_init(drain, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&xfull[i], 1);
-            mbar_init(&cfree[i], WORKERS);
-            mbar_init(&xfree[i], 1);
             mbar_init(&dfull[i], 1);
             mbar_init(&dready[i], WORKERS);
             mbar_init(&dfree[i], 1);
@@ -233,9 +239,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             for (int u = 0; ok && u < units; ++u) {
                 const int t = u / CHUNKS, c = u - t * CHUNKS;
                 if (c == 0) {
-                    const int xb = t & 1;
-                    uint64_t *fr = kHeld8 ? &cfree[xb] : &xfree[xb];
-                    if (t >= 2 && !(ok = wait_bounded(fr, (uint32_t)((t >> 1) - 1) & 1u, abort_flag, ctl, SITE_LBW | 1, t))) break;
+                    const int xb = t % XB;
+                    if (t >= XB && !(ok = wait_bounded(&xfree[xb], (uint32_t)(t / XB - 1) & 1u, abort_flag, ctl, SITE_LBW | 1, t))) break;
                     if (kHeld8) {
                         mbar_arrive_expect_tx(&xfull[xb], CODES);
                         tma_load_3d(codes + xb * CODES, &tmX, &xfull[xb], 0, row0(t), 0);
@@ -255,11 +260,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             }
             // No copy may be in flight when the CTA leaves.
             wait_drain(wfull, 0, ctl.timeout_ns);
-            for (int i = 0; i < 2; ++i) {
-                const int nx = (xs + 1 - i) / 2, nd = (ds + 1 - i) / 2;  // phases of buffer i
-                if (nx > 0) wait_drain(&xfull[i], (uint32_t)(nx - 1) & 1u, ctl.timeout_ns);
-                if (nd > 0) wait_drain(&dfull[i], (uint32_t)(nd - 1) & 1u, ctl.timeout_ns);
-            }
+            for (int x = max(0, xs - XB); x < xs; ++x) wait_drain(&xfull[x % XB], (uint32_t)(x / XB) & 1u, ctl.timeout_ns);
+            for (int d = max(0, ds - 2); d < ds; ++d) wait_drain(&dfull[d & 1], (uint32_t)(d >> 1) & 1u, ctl.timeout_ns);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -267,10 +269,10 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             const uint32_t i_p = idesc_bf16(128, 128, 0, 0), i_dx = idesc_bf16(128, 128, 0, 1), i_dw = idesc_bf16(128, 128, 1, 1);
             const uint32_t w0 = smem_u32(wbuf), x0 = smem_u32(xbuf), d0 = smem_u32(dbuf);
             ok = wait_bounded(wfull, 0, abort_flag, ctl, SITE_LBW | 3, 0);
-            auto xtile = [&](int t) { return x0 + (kHeld8 ? 0u : (uint32_t)((t & 1) * TILE)); };
+            auto xtile = [&](int t) { return x0 + (kHeld8 ? 0u : (uint32_t)((t % XB) * TILE)); };
             auto wait_x = [&](int t) {
                 if (kHeld8) return wait_bounded(xready, (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 4, t);
-                return wait_bounded(&xfull[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 4, t);
+                return wait_bounded(&xfull[t % XB], (uint32_t)(t / XB) & 1u, abort_flag, ctl, SITE_LBW | 4, t);
             };
             // p of unit u, once x is there and the accumulator has been read.
             auto issue_p = [&](int u) {
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 }
                 mma_commit(&dfree[db]);
                 if (c == CHUNKS - 1) {
-                    mma_commit(&xfree[kHeld8 ? 0 : t & 1]);
+                    mma_commit(kHeld8 ? xdone : &xfree[t % XB]);
                     mma_commit(dxfull);
                 }
                 if (has_p && u + 1 < units && wait_for_x && !(ok = issue_p(u + 1))) break;
@@ -350,12 +352,12 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         };
         uint32_t scale_next = kHeld8 ? scale_of(0) : 0u;
         auto convert = [&](int t) {
-            if (!warp_wait(&xfull[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 8, t)) return false;
-            if (t > 0 && !warp_wait(&xfree[0], (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 9, t)) return false;
+            if (!warp_wait(&xfull[t % XB], (uint32_t)(t / XB) & 1u, abort_flag, ctl, SITE_LBW | 8, t)) return false;
+            if (t > 0 && !warp_wait(xdone, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 9, t)) return false;
             const uint32_t s = scale_next;
             scale_next = scale_of(t + 1);
             const float size = __uint_as_float(s ? s << 23 : 0x00400000u);  // 2^(s - 127)
-            const uint8_t *src = codes + (t & 1) * CODES + crow * 128;
+            const uint8_t *src = codes + (t % XB) * CODES + crow * 128;
             uint8_t *dst = xbuf + (cblk >> 1) * HALF + crow * 128;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&cfree[t & 1]);
+                mbar_arrive(&xfree[t % XB]);
                 mbar_arrive(xready);
             }
             return true;
@@ -428,9 +430,9 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 }
                 if (__any_sync(0xffffffffu, check != 0)) {
                     // x and W are read here as they landed: observe their barriers.
-                    uint64_t *xb = kHeld8 ? xready : &xfull[t & 1];
+                    uint64_t *xb = kHeld8 ? xready : &xfull[t % XB];
                     if (!warp_wait(wfull, 0, abort_flag, ctl, SITE_LBW | 14, u) ||
-                        !warp_wait(xb, (uint32_t)(kHeld8 ? t : t >> 1) & 1u, abort_flag, ctl, SITE_LBW | 14, u))
+                        !warp_wait(xb, (uint32_t)(kHeld8 ? t : t / XB) & 1u, abort_flag, ctl, SITE_LBW | 14, u))
                         return false;
                 }
                 for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                         const int bit = __ffs(left) - 1, i = bit >> 1;
                         const int r = 32 * q + 16 * (i >> 3) + 8 * (i & 1) + (src >> 2);
                         const int col = 32 * h + 8 * ((i >> 1) & 3) + 2 * (src & 3) + (bit & 1);
-                        const uint2 xv = tile_quad(xbuf + (kHeld8 ? 0 : (t & 1) * TILE), r, lane), wv = tile_quad(wbuf + c * TILE, col, lane);
+                        const uint2 xv = tile_quad(xbuf + (kHeld8 ? 0 : (t % XB) * TILE), r, lane), wv = tile_quad(wbuf + c * TILE, col, lane);
                         const float2 xa = two(xv.x), xb = two(xv.y), wa = two(wv.x), wb = two(wv.y);
                         double sum = (double)xa.x * wa.x + (double)xa.y * wa.y + (double)xb.x * wb.x + (double)xb.y * wb.y;
 #pragma unroll
@@ -615,7 +617,7 @@ namespace {
 template <int CHUNKS, bool kPair, bool kHeld8, int ACT>
 cudaError_t allow() {
     return cudaFuncSetAttribute(linear_bwd_kernel<CHUNKS, kPair, kHeld8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)lb::smem(CHUNKS));
+                                (int)lb::SMEM);
 }
 template <int CHUNKS, bool kPair, bool kHeld8>
 cudaError_t allow_acts() {
@@ -630,7 +632,7 @@ cudaError_t go(const LinearBwdMaps &m, const LinearBwdArgs &a, int teams, cudaSt
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(kPair ? 2 * teams : teams));
     cfg.blockDim = dim3(lb::THREADS);
-    cfg.dynamicSmemBytes = lb::smem(CHUNKS);
+    cfg.dynamicSmemBytes = lb::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
