@@ -436,39 +436,43 @@ def atomattn_backward(params: AtomAttnParams, dout, grads: AtomAttnGrads, stream
     return rc
 
 
-def _need_bf16(what: str, index: int, *tensors):
-    """Every tensor (None passes) must be contiguous bf16 on CUDA device `index`."""
+# torch and what the calls below need of it, and the library: looked up by the first of them. Small
+# calls are bound by the host, so these functions keep names, attributes and allocations few.
+_T = _L = _BF16 = _U8 = _current_device = _raw_stream = None
+
+
+def _load():
+    global _T, _L, _BF16, _U8, _current_device, _raw_stream
     import torch
+    _L = lib()
+    _BF16, _U8 = torch.bfloat16, torch.uint8
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _T = torch
+    return torch
+
+
+def _need_bf16(what: str, index: int, tensors):
+    """Every tensor (None passes) must be contiguous bf16 on CUDA device `index`."""
     if index < 0:
         raise ValueError(f"{what}: tensors must be on a CUDA device")
-    bf16 = torch.bfloat16
     for t in tensors:
-        if t is None:
-            continue
-        if t.dtype is not bf16 or not t.is_contiguous():
-            raise ValueError(f"{what}: tensors must be contiguous bf16")
-        if t.get_device() != index:
-            raise ValueError(f"{what}: tensors must be on one CUDA device")
+        if t is not None:
+            if t.dtype is not _BF16 or not t.is_contiguous():
+                raise ValueError(f"{what}: tensors must be contiguous bf16")
+            if t.get_device() != index:
+                raise ValueError(f"{what}: tensors must be on one CUDA device")
 
 
 def _need_workspace(what: str, index: int, workspace):
-    import torch
-    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
-                                  or workspace.get_device() != index):
+    if workspace.dtype is not _U8 or not workspace.is_contiguous() or workspace.get_device() != index:
         raise ValueError(f"{what}: workspace must be contiguous uint8 on the tensors' device")
-
-
-def _elsewhere(index: int, stream) -> bool:
-    """Whether a call must change the current device or stream first."""
-    import torch
-    return stream is not None or torch.cuda.current_device() != index
 
 
 def _run_on(index: int, stream, tensors, call):
     """call() with device `index` current and, where one is given, `stream` current too, so that
     what the call allocates belongs to it. `tensors` may be another stream's: they are marked as
     used on this one, so that their memory is not handed out again before this work is done."""
-    import torch
+    torch = _T or _load()
     with torch.cuda.device(index):
         if stream is None:
             return call()
@@ -481,24 +485,18 @@ def _run_on(index: int, stream, tensors, call):
             return out
 
 
-def _raw_stream(index: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
 _status = {}  # device index -> status workspace of the calls that are given none
 
 
-def _status_workspace(like):
+def _status_workspace(index: int):
     """256 bytes for the status word of a call that the caller gave no workspace: one buffer per
     device, kept. Calls that overlap share it, which only their status notices. A first call
     inside a capture takes memory of the graph's own instead."""
-    import torch
-    ws = _status.get(like.get_device())
+    ws = _status.get(index)
     if ws is None:
-        ws = torch.zeros(256, dtype=torch.uint8, device=like.device)
-        if not torch.cuda.is_current_stream_capturing():
-            _status[like.get_device()] = ws
+        ws = _T.zeros(256, dtype=_U8, device=_T.device("cuda", index))
+        if not _T.cuda.is_current_stream_capturing():
+            _status[index] = ws
     return ws
 
 
@@ -508,28 +506,31 @@ def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=
     Arguments as for atom_attention, dout like q. Returns (dq, dk, dv, dbias), dbias None
     without bias. `workspace` (atomattn_workspace_size() bytes): where device_status finds this
     call's status; without one, calls of a device share a status word."""
-    import torch
+    torch = _T or _load()
     shape = q.shape
     if len(shape) != 4 or shape[3] != 32 or k.shape != shape or v.shape != shape or dout.shape != shape:
         raise ValueError("q, k, v, dout must be [batch, n_atoms, heads, 32] of one shape")
     B, n, H, _ = shape
-    if bias is not None and tuple(bias.shape) != (B, (n + 31) // 32, H, 32, 128):
+    if bias is not None and bias.shape != (B, (n + 31) // 32, H, 32, 128):
         raise ValueError("bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
-    if atom_mask is not None and tuple(atom_mask.shape) != (B, n):
+    if atom_mask is not None and atom_mask.shape != (B, n):
         raise ValueError("atom_mask must be [batch, n_atoms]")
     index = q.get_device()
-    _need_bf16("atom_attention_backward", index, q, k, v, dout, bias, atom_mask)
-    _need_workspace("atom_attention_backward", index, workspace)
-    if _elsewhere(index, stream):
+    _need_bf16("atom_attention_backward", index, (q, k, v, dout, bias, atom_mask))
+    if workspace is not None:
+        _need_workspace("atom_attention_backward", index, workspace)
+    if stream is not None or _current_device() != index:
         return _run_on(index, stream, (q, k, v, dout, bias, atom_mask, workspace),
                        lambda: atom_attention_backward(q, k, v, dout, bias, atom_mask, workspace))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
     dbias = None if bias is None else torch.empty_like(bias)
-    ws = _status_workspace(q) if workspace is None else workspace
-    p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask),
-                       ws.data_ptr(), ws.numel(), 0)
-    atomattn_backward(p, dout, AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dbias)),
-                      _raw_stream(index))
+    ws = _status_workspace(index) if workspace is None else workspace
+    p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), None if bias is None else bias.data_ptr(),
+                       None if atom_mask is None else atom_mask.data_ptr(), ws.data_ptr(), ws.numel(), 0)
+    g = AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if bias is None else dbias.data_ptr())
+    rc = _L.atomattn_backward(p, dout.data_ptr(), g, _raw_stream(index))
+    if rc:
+        raise TrimulError(rc, "atomattn_backward")
     return dq, dk, dv, dbias
 
 
@@ -584,7 +585,7 @@ def device_status(workspace, stream=None):
     """(code, [code, site, block, aux]) that the last linear, linear_backward or
     atom_attention_backward call with this workspace left (synchronises); with a device in the
     workspace's place, the last such call of that device that was given none."""
-    import torch
+    torch = _T or _load()
     if not isinstance(workspace, torch.Tensor):
         device = torch.device(workspace)
         index = torch.cuda.current_device() if device.index is None else device.index
@@ -604,14 +605,14 @@ class Act8:
     __slots__ = ("codes", "scales")
 
     def __init__(self, codes, scales):
-        import torch
+        _T or _load()
         shape, c = codes.shape, codes.shape[-1] if codes.dim() else 0
         if c == 0 or c % 32 or scales.shape != shape[:-1] + (c // 32,):
             raise ValueError("codes must be [..., channels] and scales [..., channels / 32]")
         for t in (codes, scales):
-            if t.dtype is not torch.uint8 or not t.is_contiguous():
+            if t.dtype is not _U8 or not t.is_contiguous():
                 raise ValueError("codes and scales must be contiguous uint8")
-        if codes.device != scales.device:
+        if codes.get_device() != scales.get_device():
             raise ValueError("codes and scales must be on one device")
         self.codes, self.scales = codes, scales
 
@@ -626,45 +627,53 @@ class Act8:
 
 def act8_pack(x, stream=None) -> Act8:
     """Keep a bf16 tensor [..., channels] (channels a multiple of 32) in 33/32 bytes per value."""
-    import torch
+    torch = _T or _load()
     shape = x.shape
-    if len(shape) < 1 or shape[-1] == 0 or shape[-1] % 32:
+    c = shape[-1] if len(shape) else 0
+    if c == 0 or c % 32:
         raise ValueError("x must be [..., channels], channels a multiple of 32")
     index = x.get_device()
-    _need_bf16("act8_pack", index, x)
-    if _elsewhere(index, stream):
+    _need_bf16("act8_pack", index, (x,))
+    if stream is not None or _current_device() != index:
         return _run_on(index, stream, (x,), lambda: act8_pack(x))
-    c = shape[-1]
-    codes = torch.empty_like(x, dtype=torch.uint8)
+    codes = torch.empty_like(x, dtype=_U8)
     scales = codes.new_empty(shape[:-1] + (c // 32,))
-    if codes.numel():
-        trimul_act8_pack(x, codes.numel() // c, c, codes, scales, _raw_stream(index))
-    return Act8(codes, scales)
+    count = codes.numel()
+    if count:
+        rc = _L.trimul_act8_pack(x.data_ptr(), count // c, c, codes.data_ptr(), scales.data_ptr(), _raw_stream(index))
+        if rc:
+            raise TrimulError(rc, "trimul_act8_pack")
+    a = Act8.__new__(Act8)  # nothing to check: these are ours
+    a.codes, a.scales = codes, scales
+    return a
 
 
 def act8_unpack(a: Act8, out=None, stream=None):
     """The values an Act8 stands for, as a bf16 tensor (written to `out` if given)."""
-    import torch
+    torch = _T or _load()
     codes, scales = a.codes, a.scales
     index = codes.get_device()
     if out is not None and out.shape != codes.shape:
         raise ValueError("out must have the codes' shape")
-    _need_bf16("act8_unpack", index, out)
-    if _elsewhere(index, stream):
+    _need_bf16("act8_unpack", index, (out,))
+    if stream is not None or _current_device() != index:
         return _run_on(index, stream, (codes, scales, out), lambda: act8_unpack(a, out))
-    x = torch.empty_like(codes, dtype=torch.bfloat16) if out is None else out
-    if x.numel():
+    x = torch.empty_like(codes, dtype=_BF16) if out is None else out
+    count = x.numel()
+    if count:
         c = codes.shape[-1]
-        trimul_act8_unpack(codes, scales, x.numel() // c, c, x, _raw_stream(index))
+        rc = _L.trimul_act8_unpack(codes.data_ptr(), scales.data_ptr(), count // c, c, x.data_ptr(), _raw_stream(index))
+        if rc:
+            raise TrimulError(rc, "trimul_act8_unpack")
     return x
 
 
 def _linear_shape(what, x_shape, weight, bias, act):
     """Shape of the layer's result."""
     w = weight.shape
-    if len(w) != 2 or len(x_shape) < 1 or x_shape[-1] != w[1]:
+    if len(w) != 2 or len(x_shape) < 1 or x_shape[-1] != w[1] or w[1] == 0:
         raise ValueError(f"{what}: x must be [..., in_features] and weight [out_features, in_features]")
-    if bias is not None and (bias.dim() != 1 or bias.shape[0] != w[0]):
+    if bias is not None and bias.shape != w[:1]:
         raise ValueError(f"{what}: bias must be [out_features]")
     if act not in ACTS:
         raise ValueError(f"{what}: act must be one of {', '.join(ACTS)}")
@@ -680,23 +689,30 @@ def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=
     recorded by autograd: linear_backward gives the gradients. `workspace`
     (trimul_linear_workspace_size() bytes): where device_status finds this call's status;
     without one, calls of a device share a status word."""
+    torch = _T or _load()
     shape = _linear_shape("linear", x.shape, weight, bias, act)
     index = x.get_device()
-    _need_bf16("linear", index, x, weight, bias, residual, out)
-    _need_workspace("linear", index, workspace)
+    _need_bf16("linear", index, (x, weight, bias, residual, out))
+    if workspace is not None:
+        _need_workspace("linear", index, workspace)
     if residual is not None and residual.shape != shape:
         raise ValueError("linear: residual must have the result's shape")
     if out is not None and out.shape != shape:
         raise ValueError("linear: out must have the result's shape")
-    if _elsewhere(index, stream):
+    if stream is not None or _current_device() != index:
         return _run_on(index, stream, (x, weight, bias, residual, out, workspace),
                        lambda: linear(x, weight, bias, residual, act, out, workspace))
-    y = x.new_empty(shape) if out is None else out
-    if y.numel():
-        n, k = weight.shape
-        ws = _status_workspace(x) if workspace is None else workspace
-        p = LinearParams(y.numel() // n, k, n, ACTS[act], weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
-        trimul_linear_forward(x, residual, p, y, _raw_stream(index))
+    n, k = weight.shape
+    y = out if out is not None else torch.empty_like(x) if n == k else x.new_empty(shape)
+    rows = x.numel() // k
+    if rows and n:
+        ws = _status_workspace(index) if workspace is None else workspace
+        p = LinearParams(rows, k, n, ACTS[act], weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                         ws.data_ptr(), ws.numel(), 0)
+        rc = _L.trimul_linear_forward(x.data_ptr(), None if residual is None else residual.data_ptr(), p, y.data_ptr(),
+                                      _raw_stream(index))
+        if rc:
+            raise TrimulError(rc, "trimul_linear_forward")
     return y
 
 
@@ -708,22 +724,23 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
     and comes back as None; db is computed without bias too (a bias of zeros). The
     residual's gradient is dout itself. `workspace`: trimul_linear_backward_workspace_size
     bytes, for callers that keep one or want the call's status (device_status)."""
-    import torch
+    torch = _T or _load()
     held = isinstance(x, Act8)
     shape = _linear_shape("linear_backward", x.shape, weight, bias, act)
     if dout.shape != shape:
         raise ValueError("linear_backward: dout must be [..., out_features] with x's leading dimensions")
     index = weight.get_device()
-    _need_bf16("linear_backward", index, weight, None if held else x, dout, bias)
-    _need_workspace("linear_backward", index, workspace)
+    _need_bf16("linear_backward", index, (weight, None if held else x, dout, bias))
+    if workspace is not None:
+        _need_workspace("linear_backward", index, workspace)
     if held and x.codes.get_device() != index:
         raise ValueError("linear_backward: tensors must be on one CUDA device")
-    if _elsewhere(index, stream):
+    if stream is not None or _current_device() != index:
         tensors = (x.codes, x.scales) if held else (x,)
         return _run_on(index, stream, tensors + (weight, dout, bias, workspace),
                        lambda: linear_backward(x, weight, dout, bias, act, need_dx, need_dw, need_db, workspace))
     n, k = weight.shape
-    dx = None if not need_dx else torch.empty_like(x) if not held else weight.new_empty(x.shape)
+    dx = None if not need_dx else torch.empty_like(x) if not held else torch.empty_like(x.codes, dtype=_BF16)
     dw = torch.empty_like(weight) if need_dw else None
     db = None if not need_db else torch.empty_like(bias) if bias is not None else weight.new_empty(n)
     rows = dout.numel() // n if n else 0
@@ -732,17 +749,18 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
             if t is not None:
                 t.zero_()
         return dx, dw, db
-    code = ACTS[act]
-    ws = workspace
+    code, ws = ACTS[act], workspace
     if ws is None:
-        need = trimul_linear_backward_workspace_size(rows, k, n, code, held)
-        ws = _status_workspace(weight) if need <= 256 else weight.new_empty(need, dtype=torch.uint8)
-    p = LinearParams(rows, k, n, code, weight.data_ptr(), _ptr(bias), ws.data_ptr(), ws.numel(), 0)
-    if held:
-        trimul_linear_backward(None, Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()), dout, p, dx, dw, db,
-                               _raw_stream(index))
-    else:
-        trimul_linear_backward(x, None, dout, p, dx, dw, db, _raw_stream(index))
+        need = _L.trimul_linear_backward_workspace_size(rows, k, n, code, held)
+        ws = _status_workspace(index) if need <= 256 else weight.new_empty(need, dtype=_U8)
+    p = LinearParams(rows, k, n, code, weight.data_ptr(), None if bias is None else bias.data_ptr(), ws.data_ptr(),
+                     ws.numel(), 0)
+    rc = _L.trimul_linear_backward(None if held else x.data_ptr(),
+                                   Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()) if held else None, dout.data_ptr(), p,
+                                   dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
+                                   db.data_ptr() if need_db else None, _raw_stream(index))
+    if rc:
+        raise TrimulError(rc, "trimul_linear_backward")
     return dx, dw, db
 
 

@@ -1830,7 +1830,7 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     uint8_t *base = static_cast<uint8_t *>(p->workspace);
     const KernelCtl ctl = linear_ctl(p);
     if ((dx || dw || db) && linear_one_pass(k, n)) return run_linear_one_pass(x, x8, dy, p, dx, dw, db, L, ctl, s);
-    if ((rc = cuda_rc(cudaMemsetAsync(base, 0, sizeof(DeviceStatus), s), "status clear"))) return rc;
+    bool clear = true;  // the call's first tensor kernel clears the status word
     const bool d_pass = act != TRIMUL_ACT_NONE && (dx || dw || db);
     if (x8 && (dw || db || d_pass)) {
         if ((rc = cuda_rc(launch_act8_unpack(codes, scales, base + L.x, rows * k, d->sms, s), "act8_unpack launch")))
@@ -1844,19 +1844,25 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     if (d_pass) {
         int groups = 0;
         if ((rc = run_linear(LIN_GRAD, x, p->weight, 0, dy, base + L.d, (int)rows, n, k, act, p->bias,
-                             db ? sums : nullptr, false, &groups, ctl, *d, s)))
+                             db ? sums : nullptr, clear, &groups, ctl, *d, s)))
             return rc;
+        clear = false;
         D = base + L.d;
         sum_rows = 4 * groups;
     }
-    if (dx && (rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr,
-                               false, nullptr, ctl, *d, s)))
-        return rc;
+    if (dx) {
+        if ((rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr, clear,
+                             nullptr, ctl, *d, s)))
+            return rc;
+        clear = false;
+    }
     const bool rows_sum = db && !d_pass;  // D is dy: its sums come with the weight product
     if (dw || rows_sum) {
-        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, rows_sum ? sums : nullptr, false, ctl, *d, s)))
+        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, rows_sum ? sums : nullptr, clear, ctl, *d, s)))
             return rc;
+        clear = false;
     }
+    if (clear && (rc = cuda_rc(cudaMemsetAsync(base, 0, sizeof(DeviceStatus), s), "status clear"))) return rc;
     LinearReduceArgs r;
     memset(&r, 0, sizeof r);
     r.partial = partial;
