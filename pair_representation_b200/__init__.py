@@ -918,3 +918,87 @@ class TriangleMultiplicationOutgoing(_TriangleMultiplication):
 class TriangleMultiplicationIncoming(_TriangleMultiplication):
     """x_ij = sum_k a_ki * b_kj."""
     direction = INCOMING
+
+
+# ---- the atom attention as a trainable layer ---------------------------------
+
+class AtomAttention:
+    """Windowed atom attention with its projections: x + W_o attention(W_q x, W_k x, W_v x) + b_o.
+
+    x: [batch, n_atoms, c_atom] bf16; heads of 32 channels; bias and atom_mask as for
+    atom_attention. The projections and the residual run in `linear`, the core in
+    atom_attention; ``backward`` runs linear_backward and atom_attention_backward and keeps
+    nothing of the forward but x, which may have been kept in 8 bits (act8_pack)."""
+
+    KEYS = tuple(f"linear_{n}.{p}" for n in "qkvo" for p in ("weight", "bias"))
+
+    def __init__(self, c_atom: int = 128, heads: int = 4):
+        self.c_atom, self.heads = c_atom, heads
+        self.tensors = {}
+
+    def load_state_dict(self, sd: dict):
+        """Take linear_q, linear_k, linear_v, linear_o .weight ([heads * 32, c_atom], o transposed) and,
+        where present, .bias."""
+        import torch
+        c, d = self.c_atom, self.heads * 32
+        t = {}
+        for key in self.KEYS:
+            out, inn = (c, d) if key.startswith("linear_o") else (d, c)
+            if sd.get(key) is None:
+                if key.endswith("weight"):
+                    raise KeyError(key)
+                continue
+            v = sd[key] if isinstance(sd[key], torch.Tensor) else torch.as_tensor(sd[key])
+            if tuple(v.shape) != ((out, inn) if key.endswith("weight") else (out,)):
+                raise ValueError(f"{key}: shape {tuple(v.shape)}")
+            t[key] = v
+        self.tensors = t
+        return self
+
+    def to(self, device=None, dtype=None):
+        import torch
+        if dtype not in (None, torch.bfloat16):
+            raise ValueError("dtype must be bfloat16")
+        self.tensors = {k: v.to(device=device, dtype=torch.bfloat16).contiguous() for k, v in self.tensors.items()}
+        return self
+
+    def _linear(self, name, x, residual=None):
+        return linear(x, self.tensors[f"linear_{name}.weight"], self.tensors.get(f"linear_{name}.bias"), residual)
+
+    def _core(self, x, bias, atom_mask):
+        shape = tuple(x.shape[:2]) + (self.heads, 32)
+        q, k, v = (self._linear(n, x).view(shape) for n in "qkv")
+        return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
+
+    def _check(self, x):
+        if len(x.shape) != 3 or x.shape[2] != self.c_atom:
+            raise ValueError("x must be [batch, n_atoms, c_atom]")
+
+    def __call__(self, x, bias=None, atom_mask=None):
+        self._check(x)
+        o = self._core(x, bias, atom_mask)[3]
+        return self._linear("o", o.view(*x.shape[:2], self.heads * 32), residual=x)
+
+    def backward(self, x, dout, bias=None, atom_mask=None):
+        """Gradients of sum(layer(x, bias, atom_mask) * dout): (dx, dbias, {state-dict key: gradient}).
+
+        x is the forward's input or the Act8 that kept it (the gradients are then those at the values it
+        stands for). q, k, v and the attention's output are recomputed from it. Every parameter gets a
+        gradient, biases the state dict left out included."""
+        self._check(x)
+        held = isinstance(x, Act8)
+        q, k, v, o = self._core(act8_unpack(x) if held else x, bias, atom_mask)
+        rows = tuple(x.shape[:2]) + (self.heads * 32,)
+        grads = {}
+
+        def back(name, inp, d):
+            dx, grads[f"linear_{name}.weight"], grads[f"linear_{name}.bias"] = linear_backward(
+                inp, self.tensors[f"linear_{name}.weight"], d, self.tensors.get(f"linear_{name}.bias"))
+            return dx
+
+        do = back("o", o.view(rows), dout).view(o.shape)
+        dq, dk, dv, dbias = atom_attention_backward(q, k, v, do, bias, atom_mask)
+        dx = dout.float()  # the residual's gradient; the four are added in fp32 and rounded once
+        for name, d in (("q", dq), ("k", dk), ("v", dv)):
+            dx += back(name, x, d.view(rows))
+        return dx.to(dout.dtype), dbias, grads
