@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                         mma_bf16(tmem + 128 * c, sdesc_sw128(dt + j * 2048, HALF, 1024), sdesc_sw128(xtile(t) + j * 2048, HALF, 1024),
                                  i_dw, (t | j) ? 1u : 0u);
                 }
+                if (c == CHUNKS - 1) mma_commit(kHeld8 ? xdone : &xfree[t % XB]);  // the last product that reads x
                 if (args.has_dx) {
                     if (c == 0 && t > 0) {
                         if (!(ok = wait_bounded(dxfree, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 7, t))) break;
@@ -313,10 +314,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                                  sdesc_sw128(w0 + c * TILE + j * 2048, HALF, 1024), i_dx, (c | j) ? 1u : 0u);
                 }
                 mma_commit(&dfree[db]);
-                if (c == CHUNKS - 1) {
-                    mma_commit(kHeld8 ? xdone : &xfree[t % XB]);
-                    mma_commit(dxfull);
-                }
+                if (c == CHUNKS - 1) mma_commit(dxfull);
                 if (has_p && u + 1 < units && wait_for_x && !(ok = issue_p(u + 1))) break;
             }
             mma_commit(drain);
@@ -523,8 +521,9 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         const bool has_dx = args.has_dx != 0;
         for (int t = 0; ok && t < my_tiles; ++t) {
             if (kHeld8) {
-                if (has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
+                // x first: p of the tile is then computed while dx of the tile before is drained.
                 if (!(ok = convert(t))) break;
+                if (has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
             }
             for (int c = 0; c < CHUNKS; ++c) {
                 if (!(ok = make_d(t * CHUNKS + c))) break;
