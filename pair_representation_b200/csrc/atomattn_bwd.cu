@@ -366,13 +366,6 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         // Every warp's part is there; and every warp is done with the window before.
         ok = __syncthreads_and(ok);
         if (!ok) break;
-        if (threadIdx.x == 0 && i > 0 && first + issued < wend) {
-            // The stage of window s - 1 and the ring slot of group s - 1 are free once the copy of its dbias
-            // has read the tile.
-            tma_store_wait_read<0>();
-            issue(first + issued);
-            ++issued;
-        }
         if (pos == 0) key = key_bits(s + 4);  // the warp's next group
         float2 *rowv = reinterpret_cast<float2 *>(smem + OFF_ROW) + warp * 32;
         {
@@ -415,6 +408,14 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         }
         fence_proxy_async_smem();
         __syncthreads();  // P and dS of all 128 slots are in their tiles
+        if (threadIdx.x == 0 && i > 0 && first + issued < wend) {
+            // The stage of window s - 1 and the ring slot of group s - 1 have been free since the barrier before
+            // this one, once the copy of its dbias has read the tile. Issued here, where no warp waits for this
+            // one, a window and a half still passes before the data is needed.
+            tma_store_wait_read<0>();
+            issue(first + issued);
+            ++issued;
+        }
         if (threadIdx.x == 32) {
             // dv += P^T dO, dk += dS^T q: 128 keys (group g mod 4 in lanes 32 (g mod 4) ..) x 32 channels,
             // K = 32 queries in two steps; tiles of 32 keys are 2 KB apart.
