@@ -1150,13 +1150,14 @@ int check_attn_backward(const atomattn_params *p, const void *dout, const atomat
     return TRIMUL_OK;
 }
 
-// q, k or v [batch][n][heads][32] as (heads * 32, n, batch): boxes of one head's 32 elements x `rows`.
-int map_attn(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t rows) {
+// q, k or v [batch][n][heads][32] as (heads * 32, n, batch): boxes of one head's 32 elements
+// (or 16 of them) x `rows`.
+int map_attn(CUtensorMap *m, const void *t, const atomattn_params *p, uint32_t rows, uint32_t channels = 32) {
     const uint64_t row = (uint64_t)p->heads * 32;
     const uint64_t dims[3] = {row, (uint64_t)p->n_atoms, (uint64_t)p->batch};
     const uint64_t strides[2] = {row * 2, row * 2 * (uint64_t)p->n_atoms};
-    const uint32_t box[3] = {32, rows, 1};
-    return encode(m, 3, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+    const uint32_t box[3] = {channels, rows, 1};
+    return encode(m, 3, t, dims, strides, box, channels == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 // bias [batch][n_windows][heads][32][128] as (slot, row, head, window, batch): boxes of one
@@ -1720,7 +1721,8 @@ int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn
         return rc;
     AttnBwdMaps m;
     if ((rc = map_attn(&m.q, p->q, p, 32)) || (rc = map_attn(&m.k, p->k, p, 32)) || (rc = map_attn(&m.v, p->v, p, 32)) ||
-        (rc = map_attn(&m.dout, dout, p, 32)))
+        (rc = map_attn(&m.dout, dout, p, 32)) || (rc = map_attn(&m.dq, g->dq, p, 16, 16)) ||
+        (rc = map_attn(&m.dk, g->dk, p, 32)) || (rc = map_attn(&m.dv, g->dv, p, 32)))
         return rc;
     m.bias = m.dbias = m.q;  // unused without a bias
     if (p->bias && (rc = map_attn_bias(&m.bias, p->bias, p, 32))) return rc;
@@ -1734,7 +1736,6 @@ int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn
     a.has_bias = p->bias != nullptr;
     a.has_dbias = g->dbias != nullptr;
     a.mask = static_cast<const __nv_bfloat16 *>(p->atom_mask);
-    a.dq = static_cast<__nv_bfloat16 *>(g->dq);
     a.dk = static_cast<__nv_bfloat16 *>(g->dk);
     a.dv = static_cast<__nv_bfloat16 *>(g->dv);
     a.scale = 0.17677669529663687f;  // 1 / sqrt(32)

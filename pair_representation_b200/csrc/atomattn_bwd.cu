@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     atomattn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                         const __grid_constant__ CUtensorMap tmBias, const __grid_constant__ CUtensorMap tmDbias,
-                        const AttnBwdArgs args) {
+                        const __grid_constant__ CUtensorMap tmDq, const __grid_constant__ CUtensorMap tmDk,
+                        const __grid_constant__ CUtensorMap tmDv, const AttnBwdArgs args) {
     using namespace ab;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((512u - (smem_u32(smem_raw) & 511u)) & 511u);
@@ -219,36 +220,52 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     // ldmatrix / stmatrix lane addresses within a tile: rows as a left operand's, as a right operand's.
     const uint32_t a64 = at64((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
     const uint32_t b64 = at64((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const int s_r = (lane & 7) + ((lane >> 3) & 1) * 8;
+    const uint32_t s32 = (uint32_t)(s_r * 32 + (((lane >> 4) ^ ((s_r >> 2) & 1)) << 4));
     const int q0 = (warp & 1) * 16, c0 = (warp >> 1) * 2;  // dq: this warp's 16 queries, and 16 channels from 8 c0
     const uint32_t mytmem = tmem + ((uint32_t)(warp * 32) << 16);
     auto ring_at = [&](int base, int j) { return base + j < RING ? base + j : base + j - RING; };
 
     // dk and dv of group g, whose windows are all summed, from this warp's lanes (lane = atom); with
     // `clear` the lanes are set to 0 for the warp's next group.
-    auto write_group = [&](int g, bool clear) {
+    auto write_group = [&](int g, bool clear, uint8_t *dv_tile) {
         if (g >= s0 && g < s1) {  // warp-uniform; else another block's
-            const int atom = g * 32 - KOFF + lane;
-            const bool inside = atom >= 0 && atom < n, valid = (vmask >> lane) & 1u;
-            const size_t off = ((size_t)b * n + atom) * row_elems + h * 32;
+            const int row = g * 32 - KOFF, atom = row + lane;
+            const bool valid = (vmask >> lane) & 1u;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t v[32];
                 tmem_ld32(mytmem + (x ? DV_COL : DK_COL), v);
                 tmem_ld_wait_regs(v);
                 if (clear) tmem_zero32(mytmem + (x ? DV_COL : DK_COL));
-                if (inside) {
-                    uint4 *dst = reinterpret_cast<uint4 *>((x ? args.dv : args.dk) + off);
-                    const float f = x ? 1.f : scale;
+                const float f = x ? 1.f : scale;
+                // Through P's tile, which is free from the window's sums to the next window's P: a lane's 64 bytes
+                // straight to memory are 32 rows an instruction, and the stores' passes through L1 were a
+                // sixth of what bounds this kernel. (A block that starts before the first atom: there is
+                // one for each sequence.)
+                uint8_t *tile = (x ? dv_tile : smem + OFF_P + warp * TILE) + lane * 64;
+                __nv_bfloat16 *dst = (x ? args.dv : args.dk) + ((size_t)b * n + atom) * row_elems + h * 32;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            o[t] = valid ? pack_bf16x2(__uint_as_float(v[8 * c + 2 * t]) * f,
-                                                       __uint_as_float(v[8 * c + 2 * t + 1]) * f)
-                                         : 0u;
-                        dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    for (int t = 0; t < 4; ++t)
+                        o[t] = valid ? pack_bf16x2(__uint_as_float(v[8 * c + 2 * t]) * f,
+                                                   __uint_as_float(v[8 * c + 2 * t + 1]) * f)
+                                     : 0u;
+                    if (row >= 0)
+                        *reinterpret_cast<uint4 *>(tile + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    else if (atom >= 0 && atom < n)
+                        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            if (row >= 0 && row < n) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tmDk, smem + OFF_P + warp * TILE, h * 32, row, b);
+                    tma_store_3d(&tmDv, dv_tile, h * 32, row, b);
+                    tma_store_commit();
                 }
             }
         } else if (clear) {
@@ -281,7 +298,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
             if (pos == 3 || i == 0) {  // a new group
                 if (i > 0) {
                     tc_fence_after();
-                    write_group(s - 1, true);
+                    // No other warp writes a group now: dv takes the next warp's part of the tile.
+                    write_group(s - 1, true, smem + OFF_P + ((warp + 1) & 3) * TILE);
                 } else {
                     tmem_zero32(mytmem + DK_COL);
                     tmem_zero32(mytmem + DV_COL);
@@ -363,6 +381,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                 if (quad == x) red[warp * 32 + 8 * x + grp] = make_float4(mx, tsum, tdot, 0.f);
             }
         }
+        // This warp's copies out of shared memory (the window before's dq, its group's dk and dv) have read it.
+        if (lane == 0) tma_store_wait_read<0>();
         // Every warp's part is there; and every warp is done with the window before.
         ok = __syncthreads_and(ok);
         if (!ok) break;
@@ -410,9 +430,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         __syncthreads();  // P and dS of all 128 slots are in their tiles
         if (threadIdx.x == 0 && i > 0 && first + issued < wend) {
             // The stage of window s - 1 and the ring slot of group s - 1 have been free since the barrier before
-            // this one, once the copy of its dbias has read the tile. Issued here, where no warp waits for this
-            // one, a window and a half still passes before the data is needed.
-            tma_store_wait_read<0>();
+            // this one. Issued here, where no warp waits for this one, a window still passes before the data is
+            // needed.
             issue(first + issued);
             ++issued;
         }
@@ -452,14 +471,20 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                     mma_next(dq[1], a, bk[2], bk[3]);
                 }
             }
+            // Out through the slot of v of the group that has just seen its last scores: 512 bytes a warp, rows of 32
+            // bytes with the 32-byte swizzle.
+            uint32_t o[2][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int atom = s * QW + q0 + 8 * r + grp;
-                if (atom < n) {
-                    __nv_bfloat16 *dst = args.dq + ((size_t)b * n + atom) * row_elems + h * 32 + c0 * 8 + 2 * quad;
-                    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(dq[0][r].x * scale, dq[0][r].y * scale);
-                    *reinterpret_cast<uint32_t *>(dst + 8) = pack_bf16x2(dq[1][r].x * scale, dq[1][r].y * scale);
-                }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) o[x][r] = pack_bf16x2(dq[x][r].x * scale, dq[x][r].y * scale);
+            uint8_t *out = smem + OFF_V + base * TILE + warp * 512;
+            stsm4(smem_u32(out) + s32, o[0][0], o[0][1], o[1][0], o[1][1]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && s * QW + q0 < n) {
+                tma_store_3d(&tmDq, out, h * 32 + c0 * 8, s * QW + q0, b);
+                tma_store_commit();
             }
         }
         if (++st == kStages) {
@@ -473,18 +498,18 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         const int last = wend - 1;
         if (warp_wait(summed, (uint32_t)(last - first) & 1u, abort_flag, ctl, SITE_ATB | 3, last)) {
             tc_fence_after();
-            write_group(last + ((warp - last) & 3), false);
+            // Here up to three warps do: dv takes the warp's part of the bias tile that no window needs any more.
+            write_group(last + ((warp - last) & 3), false, smem + OFF_BIAS + st * BIAS + warp * TILE);
         }
     } else if (threadIdx.x == 32) {
         mma_commit(drain);  // no product may still be running when the block leaves
         wait_drain(drain, 0, ctl.timeout_ns);
     }
-    if (threadIdx.x == 0) {
-        // No copy may be in flight when the block leaves (loads: only after a timeout).
+    // No copy may be in flight when the block leaves (loads: only after a timeout).
+    if (threadIdx.x == 0)
         for (int x = max(0, issued - kStages); x < issued; ++x)
             wait_drain(&full[x % kStages], (uint32_t)(x / kStages) & 1u, ctl.timeout_ns);
-        tma_store_wait_all<0>();
-    }
+    if (lane == 0) tma_store_wait_all<0>();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -507,7 +532,8 @@ cudaError_t launch_atomattn_bwd(const AttnBwdMaps &m, AttnBwdArgs a, int sms, cu
     if (chains > steps) chains = steps;
     a.per_chain = (int)((steps + chains - 1) / chains);
     a.chains = (steps + a.per_chain - 1) / a.per_chain;
-    atomattn_bwd_kernel<<<(unsigned)(pairs * a.chains), ab::THREADS, ab::SMEM, s>>>(m.q, m.k, m.v, m.dout, m.bias, m.dbias, a);
+    atomattn_bwd_kernel<<<(unsigned)(pairs * a.chains), ab::THREADS, ab::SMEM, s>>>(m.q, m.k, m.v, m.dout, m.bias, m.dbias, m.dq,
+                                                                                     m.dk, m.dv, a);
     return cudaGetLastError();
 }
 

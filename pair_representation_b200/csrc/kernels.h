@@ -272,7 +272,7 @@ struct AttnBwdArgs {
     int batch, n, heads, n_windows;
     int has_bias, has_dbias;
     const __nv_bfloat16 *mask;        // [batch][n] or null
-    __nv_bfloat16 *dq, *dk, *dv;      // [batch][n][heads][32]
+    __nv_bfloat16 *dk, *dv;           // [batch][n][heads][32]
     float scale;                      // 1 / sqrt(32)
     int per_chain, chains;            // set by the launcher: key groups per block, blocks per (batch, head)
     KernelCtl ctl;
@@ -281,6 +281,8 @@ struct AttnBwdArgs {
 struct AttnBwdMaps {
     CUtensorMap q, k, v, dout;  // 3-D (heads * 32, n, batch), boxes (32, 32, 1), swizzle 64B
     CUtensorMap bias, dbias;    // 5-D as AttnMaps::bias, boxes (32, 32, 1, 1, 1), swizzle 64B
+    CUtensorMap dq;             // as q, boxes (16, 16, 1), swizzle 32B
+    CUtensorMap dk, dv;         // as q
 };
 
 cudaError_t atomattn_bwd_setup();
