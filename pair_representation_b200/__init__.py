@@ -744,8 +744,8 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
     dw = torch.empty_like(weight) if need_dw else None
     db = None if not need_db else torch.empty_like(bias) if bias is not None else weight.new_empty(n)
     rows = dout.numel() // n if n else 0
-    if rows == 0:  # nothing to sum over
-        for t in (dw, db):
+    if rows == 0:  # no rows, or no columns: nothing to sum over
+        for t in (dx, dw, db):
             if t is not None:
                 t.zero_()
         return dx, dw, db

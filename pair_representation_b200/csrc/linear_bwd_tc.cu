@@ -426,6 +426,13 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                     keep |= ((p[i].x > 0.f ? 1u : 0u) | (p[i].y > 0.f ? 2u : 0u)) << (2 * i);
                     check |= ((fabsf(p[i].x) < near_ ? 1u : 0u) | (fabsf(p[i].y) < near_ ? 2u : 0u)) << (2 * i);
                 }
+                // Rows and columns outside the matrices (p = 0 there) have nothing to decide.
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (c * 128 + 32 * h + 8 * x >= n_mine) check &= ~(0x000F000Fu << (4 * x));  // column block x
+                    const uint32_t row_bits = 0x3333u << (2 * (x & 1)) << (16 * (x >> 1));       // rows 8 x + lane / 4
+                    if ((long long)row0(t) + 32 * q + 8 * x + (lane >> 2) >= args.rows) check &= ~row_bits;
+                }
                 if (__any_sync(0xffffffffu, check != 0)) {
                     // x and W are read here as they landed: observe their barriers.
                     uint64_t *xb = kHeld8 ? xready : &xfull[t % XB];

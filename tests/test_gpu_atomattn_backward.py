@@ -96,6 +96,13 @@ def test_parity(B, n, H, mask):
     check(run(*args), args)
 
 
+@pytest.mark.parametrize("n", [2049, 2080, 4000])
+def test_long_chains(n):
+    """Runs of many windows per block, and the ends of sequences inside and on group borders."""
+    args = draw(7, n, 16, seed=n)
+    check(run(*args), args)
+
+
 @pytest.mark.parametrize("mask", ["none", "gap", "one"])
 @pytest.mark.parametrize("bias", [True, False])
 def test_masks(bias, mask):

@@ -235,7 +235,9 @@ def test_leading_dimensions_empty_batches_streams_and_graphs():
     grads = tm.linear_backward(x, w, dy, bias=b, act="sigmoid")
     got = tm.linear_backward(x.view(4, 60, 64), w, dy.view(4, 60, 96), bias=b, act="sigmoid")
     assert got[0].shape == (4, 60, 64) and all(torch.equal(p.reshape(-1), q.reshape(-1)) for p, q in zip(got, grads))
-    assert tm.linear(x[:0], w).shape == (0, 96)
+    assert tm.linear(x[:0], w).shape == (0, 96) and tm.linear(x, w[:0]).shape == (240, 0)
+    dx, dw, db = tm.linear_backward(x, w[:0], dy[:, :0].contiguous())
+    assert (dx == 0).all() and dx.shape == (240, 64) and dw.shape == (0, 64) and db.shape == (0,)
     dx, dw, db = tm.linear_backward(x[:0], w, dy[:0])
     assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
     torch.cuda.synchronize()
@@ -252,6 +254,36 @@ def test_leading_dimensions_empty_batches_streams_and_graphs():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y3, y) and all(torch.equal(p, q) for p, q in zip(got, grads))
+
+
+@pytest.mark.parametrize("rows,k,n", [(20000, 128, 512), (700, 128, 392), (20000, 320, 136), (90, 128, 128)])
+@pytest.mark.parametrize("held", [False, True])
+def test_replayed_while_others_run(rows, k, n, held):
+    """Each way of the backward captured and replayed, with the forward, while the same calls run eagerly on
+    another stream and a second graph of them is replayed: all give the plain call's bits."""
+    x, w, b, dy = (dev(t) for t in draw(rows, k, n, 9))
+    xx = tm.act8_pack(x) if held else x
+    step = lambda: (tm.linear(x, w, bias=b, act="silu"), *tm.linear_backward(xx, w, dy, bias=b, act="silu"))  # noqa: E731
+    ref = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = step()
+    torch.cuda.synchronize()
+    for got in (*outs, eager):
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
 
 
 def test_refusals():
