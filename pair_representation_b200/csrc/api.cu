@@ -1186,7 +1186,8 @@ int linear_bn(long long M, int N) {
     return c128 == 2 * c256 && (long long)ceil_div(M, 128) * c256 >= kLinearCtas ? 256 : 128;
 }
 
-// The parts of dW's contraction over the rows: as many as give every SM one output tile.
+// The parts of dW's contraction over the rows: as many as give every SM one output tile; but one up to
+// 512 rows (8 K blocks), where a second launch to add the parts up costs more than their length saves.
 struct LinearSplit {
     int tiles, splits, per;  // 128 x 128 tiles of dW, parts, K blocks of 64 rows per part
 };
@@ -1195,7 +1196,7 @@ LinearSplit linear_split(long long rows, int k, int n) {
     s.tiles = ceil_div(n, 128) * ceil_div(k, 128);
     const int kb = ceil_div(rows, 64);
     int want = kLinearCtas / s.tiles;
-    if (want < 1) want = 1;
+    if (want < 1 || kb <= 8) want = 1;
     if (want > kb) want = kb;
     s.per = ceil_div(kb, want);
     s.splits = ceil_div(kb, s.per);
@@ -1211,9 +1212,15 @@ int linear_teams(long long rows, int n) {
     return tiles < most ? tiles : most;
 }
 
+// The groups of CTAs that take row tiles in turn in a product of M x N (LIN_FWD, LIN_GRAD).
+int linear_groups(long long M, int N) {
+    const int tiles = ceil_div(M, 128), groups = kLinearCtas / ceil_div(N, linear_bn(M, N));
+    return groups < tiles ? groups : tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
+}
+
 // Sections of the backward workspace (byte offsets, 256-byte aligned).
 struct LinearBwdLayout {
-    size_t x, d, partial, sums, total;
+    size_t x, d, partial, sums, scrap, total;
 };
 LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int from8) {
     LinearBwdLayout L;
@@ -1234,10 +1241,12 @@ LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int fro
         L.x = take(from8 ? (size_t)rows * k * 2 : 0);                   // the values of x8, bf16
         L.d = take(act != TRIMUL_ACT_NONE ? (size_t)rows * n * 2 : 0);  // D, bf16
         const LinearSplit s = linear_split(rows, k, n);
-        L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
-        // Column sums of D: one row per part, or four per row-tile group of the D product.
-        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * kLinearCtas : (size_t)s.splits;
+        if (s.splits > 1) L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
+        // Column sums of D: four per row-tile group of the D product, or one row per part of dW.
+        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * linear_groups(rows, n) : s.splits > 1 ? (size_t)s.splits : 0;
         L.sums = take(sums * n * 4);
+        // dW where only db is wanted and its sums come with the product.
+        L.scrap = take(s.splits == 1 && act == TRIMUL_ACT_NONE ? (size_t)n * k * 2 : 0);
     }
     L.total = off;
     return L;
@@ -1283,11 +1292,10 @@ int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
     return encode(m, 3, t, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. Returns the groups of row tiles
-// through *groups (LIN_GRAD's sums have four rows for each).
+// Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. LIN_GRAD: sums has four rows for each
+// of linear_groups(M, N), or where there is one group db itself is written too.
 int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, void *Y, int M, int N, int K, int act,
-               const void *bias, float *sums, bool clear, int *groups, const KernelCtl &ctl, const DevState &d,
-               cudaStream_t s) {
+               const void *bias, float *sums, void *db, bool clear, const KernelCtl &ctl, cudaStream_t s) {
     const int bn = linear_bn(M, N);
     LinearMaps m;
     if (int rc = map_operand(&m.a, A, K, M, false, 128)) return rc;
@@ -1304,8 +1312,7 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.row_tiles = ceil_div(M, 128);
     a.col_tiles = ceil_div(N, bn);
     a.kblocks = ceil_div(K, 64);
-    a.groups = kLinearCtas / a.col_tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
-    if (a.groups > a.row_tiles) a.groups = a.row_tiles;
+    a.groups = linear_groups(M, N);
     a.splits = 1;
     a.kb_per_split = a.kblocks;
     a.act = act;
@@ -1317,7 +1324,7 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.sums = sums;
     a.clear_status = clear ? 1 : 0;
     a.ctl = ctl;
-    if (groups) *groups = a.groups;
+    a.db_out = a.groups == 1 ? static_cast<__nv_bfloat16 *>(db) : nullptr;
     return cuda_rc(launch_linear_tc(m, a, mode, bn, a.col_tiles * a.groups, s), "linear_tc launch");
 }
 
@@ -1382,15 +1389,18 @@ int run_linear_one_pass(const void *x, const trimul_act8 *x8, const void *dy, co
     return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");
 }
 
-// partial [splits][n][k] = D_s^T X_s over the rows of split s, in fp32; with sums, also the column
-// sums of D per split.
+// partial [splits][n][k] = D_s^T X_s over the rows of split s, in fp32; with with_sums, also the column
+// sums of D per split. With one split dW and db themselves.
 int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long long rows, int k, int n, float *partial,
-                     float *sums, bool clear, const KernelCtl &ctl, const DevState &d, cudaStream_t s) {
+                     float *sums, void *dw, void *db, bool with_sums, bool clear, const KernelCtl &ctl, const DevState &d,
+                     cudaStream_t s) {
     LinearMaps m;
     if (int rc = map_operand(&m.a, D, n, (int)rows, true, 0)) return rc;
     if (int rc = map_operand(&m.b, X, k, (int)rows, true, 0)) return rc;
-    if (int rc = map_view(&m.y, {partial, (size_t)k, (size_t)n * k}, k, n, sp.splits, 32, 32, 4,
-                          CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+    const bool direct = sp.splits == 1;
+    if (int rc = direct ? map_blocks(&m.y, dw, k, n)
+                        : map_view(&m.y, {partial, (size_t)k, (size_t)n * k}, k, n, sp.splits, 32, 32, 4,
+                                   CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
         return rc;
     m.e = m.y;
     LinearArgs a;
@@ -1403,7 +1413,9 @@ int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long l
     a.kblocks = ceil_div(rows, 64);
     a.splits = sp.splits;
     a.kb_per_split = sp.per;
-    a.sums = sums;
+    a.out_bf16 = direct;
+    if (with_sums && direct) a.db_out = static_cast<__nv_bfloat16 *>(db);
+    else if (with_sums) a.sums = sums;
     a.clear_status = clear ? 1 : 0;
     a.ctl = ctl;
     const long long units = (long long)sp.splits * sp.tiles;
@@ -1788,7 +1800,7 @@ int trimul_linear_forward(const void *x, const void *residual, const trimul_line
     if ((rc = device_state(&d, true))) return rc;
     if ((rc = check_current_device({x, residual, y, p->weight, p->bias, p->workspace}, "linear pointer"))) return rc;
     return run_linear(LIN_FWD, x, p->weight, 0, residual, y, (int)p->rows, p->out_features, p->in_features, p->act,
-                      p->bias, nullptr, true, nullptr, linear_ctl(p), *d, reinterpret_cast<cudaStream_t>(stream));
+                      p->bias, nullptr, nullptr, true, linear_ctl(p), reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t trimul_linear_backward_workspace_size(long long rows, int in_features, int out_features, int act, int from8) {
@@ -1842,26 +1854,34 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     const LinearSplit sp = linear_split(rows, k, n);
     const void *D = dy;
     int sum_rows = sp.splits;
+    bool db_done = false;
     if (d_pass) {
-        int groups = 0;
         if ((rc = run_linear(LIN_GRAD, x, p->weight, 0, dy, base + L.d, (int)rows, n, k, act, p->bias,
-                             db ? sums : nullptr, clear, &groups, ctl, *d, s)))
+                             db ? sums : nullptr, db, clear, ctl, s)))
             return rc;
-        clear = false;
         D = base + L.d;
+        clear = false;
+        const int groups = linear_groups(rows, n);
         sum_rows = 4 * groups;
+        db_done = groups == 1;
     }
     if (dx) {
-        if ((rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr, clear,
-                             nullptr, ctl, *d, s)))
+        if ((rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr,
+                             nullptr, clear, ctl, s)))
             return rc;
         clear = false;
     }
-    const bool rows_sum = db && !d_pass;  // D is dy: its sums come with the weight product
+    // D is dy: its sums come with the weight product.
+    const bool rows_sum = db && !d_pass;
     if (dw || rows_sum) {
-        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, rows_sum ? sums : nullptr, clear, ctl, *d, s)))
+        // One part is dW itself; where only db is wanted it goes to the workspace.
+        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, sums, dw ? dw : base + L.scrap, db, rows_sum, clear, ctl, *d, s)))
             return rc;
         clear = false;
+        if (sp.splits == 1) {
+            dw = nullptr;
+            db_done |= rows_sum;
+        }
     }
     if (clear && (rc = cuda_rc(cudaMemsetAsync(base, 0, sizeof(DeviceStatus), s), "status clear"))) return rc;
     LinearReduceArgs r;
@@ -1871,7 +1891,7 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     r.count = (long long)n * k;
     r.splits = sp.splits;
     r.sums = sums;
-    r.db = static_cast<__nv_bfloat16 *>(db);
+    r.db = db_done ? nullptr : static_cast<__nv_bfloat16 *>(db);
     r.n = n;
     r.sum_rows = sum_rows;
     return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");

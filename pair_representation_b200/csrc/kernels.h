@@ -306,13 +306,15 @@ struct LinearArgs {
     const __nv_bfloat16 *x, *w; // LIN_GRAD: A and B again, [M][K] and [N][K]
     int K;
     float *sums;  // LIN_GRAD: [groups * 4][N] column sums of Y; LIN_WG: [splits][M] row sums of A; or null
+    int out_bf16;           // LIN_WG, one split: Y is bf16
+    __nv_bfloat16 *db_out;  // LIN_GRAD with one row-tile group (beside sums), LIN_WG with one split (instead): db itself
     int clear_status;
     KernelCtl ctl;
 };
 
 struct LinearMaps {
     CUtensorMap a, b;  // 64 k x 128 rows (b: BN rows), or 64 rows x 64 k when MN-major; swizzle 128B
-    CUtensorMap e, y;  // blocks of 32 rows x 32 columns: bf16 (swizzle 64B), y of LIN_WG fp32 (swizzle 128B)
+    CUtensorMap e, y;  // blocks of 32 rows x 32 columns: bf16 (swizzle 64B), or y of LIN_WG fp32 (swizzle 128B)
 };
 
 // dw[i] = bf16(sum_s partial[s][i]), db[j] = bf16(sum_s sums[s][j]); either may be null.

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const KernelCtl &ctl = args.ctl;
-    const bool with_ones = MODE == LIN_WG && args.sums != nullptr;
+    const bool with_ones = MODE == LIN_WG && (args.sums != nullptr || args.db_out != nullptr);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -448,10 +448,22 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                 __syncwarp();
                 tmem_ld_wait_regs(v);
                 if constexpr (MODE == LIN_WG) {
+                    if (args.out_bf16) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(ob + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                o[x] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * x]), __uint_as_float(v[8 * c + 2 * x + 1]));
+                            *reinterpret_cast<uint4 *>(ob + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4 *>(ob + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                    }
                 } else {
                     const float *bias = mybias + 32 * ci;
                     float2 p[16];
@@ -483,7 +495,10 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                 tmem_ld16(lanebase + (uint32_t)(ONES_COL + 16 * acc), v);
                 tmem_ld_wait_regs(v);
                 const int row = row0 + lane;
-                if (row < args.M) args.sums[(size_t)t.split * args.M + row] = __uint_as_float(v[0]);
+                if (row < args.M) {
+                    if (args.db_out) args.db_out[row] = __float2bfloat16_rn(__uint_as_float(v[0]));
+                    else args.sums[(size_t)t.split * args.M + row] = __uint_as_float(v[0]);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -507,6 +522,14 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+    if (MODE == LIN_GRAD && args.db_out != nullptr) {
+        // The only CTA of its columns: the four quarters' sums (written before the barrier above) give db.
+        const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
+        for (int i = threadIdx.x; i < BN && n0 + i < args.N; i += THREADS) {
+            const float *sum = args.sums + n0 + i;
+            args.db_out[n0 + i] = __float2bfloat16_rn((sum[0] + sum[args.N]) + (sum[2 * (size_t)args.N] + sum[3 * (size_t)args.N]));
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
