@@ -22,7 +22,9 @@
  * Precision: bf16 operands on tcgen05 tensor cores, fp32 accumulation, bias,
  * activation and residual in fp32, one rounding to bf16 at the end. The backward
  * rounds D to bf16 before it enters the products dx and dW (with identity or relu
- * D is dy or 0, exactly); db sums D before that rounding. Gradients have the
+ * D is dy or 0, exactly); db sums D before that rounding. Where p is so near 0
+ * that fp32 cannot tell its sign (judged by the size of its row's sums), relu'
+ * takes p again in 64 bits. Gradients have the
  * parameters' type. Every sum is taken in a fixed order, so equal calls give equal
  * bits.
  *

@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             const int t = u / CHUNKS, c = u - t * CHUNKS, a = u % PRE, db = u & 1;
             give_room();
             float2 p[16];  // [16-row half][8-column block][row, row + 8]
+            float top = 0.f;  // relu: the largest sum, before its bias
             if (has_p) {
                 if (!warp_wait(&pfull[a], (uint32_t)(u / PRE) & 1u, abort_flag, ctl, SITE_LBW | 10, u)) return false;
                 tc_fence_after();
@@ -405,7 +406,9 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                     for (int x = 0; x < 4; ++x) {
                         float2 &y = p[(x >> 1) * 8 + 2 * j + (x & 1)];
                         const uint32_t *r = &v[x >> 1][4 * j + 2 * (x & 1)];
-                        y = __fadd2_rn(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])), bv);
+                        const float2 sum = make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+                        if (ACT == LIN_RELU) top = fmaxf(top, fmaxf(fabsf(sum.x), fabsf(sum.y)));
+                        y = __fadd2_rn(sum, bv);
                     }
                 }
             }
@@ -415,11 +418,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             uint32_t keep = 0xFFFFFFFFu;  // relu: bit 2 i + e of value p[i].x or .y
             if (ACT == LIN_RELU) {
                 // The sign of a p next to 0 is taken again in 64 bits (see linear_tc.cu).
-                float top = 0.f;
                 uint32_t check = 0;
                 keep = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, fmaxf(fabsf(p[i].x), fabsf(p[i].y)));
                 const float near_ = top * (16.f * 2.384185791015625e-7f);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {

@@ -303,3 +303,20 @@ def test_refusals():
               lambda: tm.linear(dy, dev(np.eye(32)), out=dy)):
         with pytest.raises(tm.TrimulError):
             f()
+
+
+@pytest.mark.parametrize("k,n", [(128, 128), (128, 512), (160, 136)])
+def test_relu_sign_under_a_large_bias(k, n):
+    """Sums near 1000 that the bias takes back to 0: fp32's rounding is then larger than many p, and the
+    gradient is still that of the exact sign. dy is 1 or -1, so db is a whole number under 256 and exact."""
+    rng = np.random.default_rng([k, n, 31])
+    x, w = rng.standard_normal((500, k)) * 0.01, rng.standard_normal((n, k))
+    x[:, 0], w[:, 0] = 1000, 1
+    x, w, b = as_bf16(x), as_bf16(w), np.full(n, -1000.0, np.float32)
+    dy = rng.choice([-1.0, 1.0], size=(500, n)).astype(np.float32)
+    p = x.astype(np.float64) @ w.astype(np.float64).T + b
+    assert (np.abs(p) < 1000 * 2.0 ** -23).sum() > 0
+    db = tm.linear_backward(dev(x), dev(w), dev(dy), bias=dev(b), act="relu")[2]
+    ref = np.where(p > 0, dy, 0).sum(axis=0)
+    assert np.abs(ref).max() <= 256
+    assert np.array_equal(db.double().cpu().numpy(), ref)
