@@ -342,9 +342,10 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                     const uint32_t two = vmask >> (8 * nt + 2 * quad);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        float2 &l = sc[x >> 1][nt][x & 1];
-                        if (!(two & 1u)) l.x = -INFINITY;
-                        if (!(two & 2u)) l.y = -INFINITY;
+                        // dP too: where every key is masked, dO may hold anything, and P = 0 would not hide it.
+                        float2 &l = sc[x >> 1][nt][x & 1], &d = dp[x >> 1][nt][x & 1];
+                        if (!(two & 1u)) l.x = -INFINITY, d.x = 0.f;
+                        if (!(two & 2u)) l.y = -INFINITY, d.y = 0.f;
                     }
                 }
             }

@@ -210,3 +210,18 @@ def test_graph_and_other_stream():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, ref))
+
+
+@pytest.mark.parametrize("bias", [True, False])
+def test_what_queries_without_a_key_hold_does_not_matter(bias):
+    """Windows whose every key is masked (padding): q and dout may hold anything."""
+    q, k, v, do, b, m = draw(2, 700, 2, seed=12, bias=bias, mask="gap")
+    clean = run(q, k, v, do, b, m)
+    q, do = q.copy(), do.copy()
+    windows = [w for w in range(22) if not m[0, max(0, 32 * w - 48):32 * w + 80].any()]
+    assert len(windows) >= 4
+    for w, (x, y) in zip(windows, ((np.nan, np.nan), (1.0, np.inf), (np.inf, 1.0), (np.inf, -np.inf))):
+        q[:, 32 * w:32 * w + 32], do[:, 32 * w:32 * w + 32] = x, y
+    dirty = run(q, k, v, do, b, m)
+    for x, y in zip(clean, dirty):
+        assert x is None and y is None or np.array_equal(x, y)
