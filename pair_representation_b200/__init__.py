@@ -966,9 +966,11 @@ class AtomAttention:
         return linear(x, self.tensors[f"linear_{name}.weight"], self.tensors.get(f"linear_{name}.bias"), residual)
 
     def _core(self, x, bias, atom_mask):
+        import torch
         shape = tuple(x.shape[:2]) + (self.heads, 32)
         q, k, v = (self._linear(n, x).view(shape) for n in "qkv")
-        return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
+        with torch.cuda.device(q.device):  # atom_attention runs on the current device
+            return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
 
     def _check(self, x):
         if len(x.shape) != 3 or x.shape[2] != self.c_atom:
