@@ -94,7 +94,8 @@ __device__ __forceinline__ uint32_t value2(uint32_t code2, float size) {
 
 __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(const uint2 *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales,
-                                                               uint4 *__restrict__ x, long long pieces) {
+                                                               uint4 *__restrict__ x, long long pieces, bool more) {
+    if (more) next_kernel_may_start();
     const long long step = (long long)gridDim.x * kThreads * kUnroll;
     for (long long base = (long long)blockIdx.x * kThreads * kUnroll + threadIdx.x; base < pieces; base += step) {
         uint2 c[kUnroll];
@@ -134,10 +135,10 @@ cudaError_t launch_act8_pack(const void *x, void *codes, void *scales, long long
     return cudaGetLastError();
 }
 
-cudaError_t launch_act8_unpack(const void *codes, const void *scales, void *x, long long values, int sms,
+cudaError_t launch_act8_unpack(const void *codes, const void *scales, void *x, long long values, int sms, bool more,
                                cudaStream_t s) {
     act8_unpack_kernel<<<grid_for(values / 8, sms), kThreads, 0, s>>>(
-        static_cast<const uint2 *>(codes), static_cast<const uint8_t *>(scales), static_cast<uint4 *>(x), values / 8);
+        static_cast<const uint2 *>(codes), static_cast<const uint8_t *>(scales), static_cast<uint4 *>(x), values / 8, more);
     return cudaGetLastError();
 }
 

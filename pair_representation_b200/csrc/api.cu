@@ -1295,7 +1295,8 @@ int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
 // Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. LIN_GRAD: sums has four rows for each
 // of linear_groups(M, N), or where there is one group db itself is written too.
 int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, void *Y, int M, int N, int K, int act,
-               const void *bias, float *sums, void *db, bool clear, const KernelCtl &ctl, cudaStream_t s) {
+               const void *bias, float *sums, void *db, bool clear, bool after, bool more, const KernelCtl &ctl,
+               cudaStream_t s) {
     const int bn = linear_bn(M, N);
     LinearMaps m;
     if (int rc = map_operand(&m.a, A, K, M, false, 128)) return rc;
@@ -1323,9 +1324,10 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.K = K;
     a.sums = sums;
     a.clear_status = clear ? 1 : 0;
+    a.more = more ? 1 : 0;
     a.ctl = ctl;
     a.db_out = a.groups == 1 ? static_cast<__nv_bfloat16 *>(db) : nullptr;
-    return cuda_rc(launch_linear_tc(m, a, mode, bn, a.col_tiles * a.groups, s), "linear_tc launch");
+    return cuda_rc(launch_linear_tc(m, a, mode, bn, a.col_tiles * a.groups, after, s), "linear_tc launch");
 }
 
 // The one-pass backward, then the sums over its teams.
@@ -1386,14 +1388,14 @@ int run_linear_one_pass(const void *x, const trimul_act8 *x8, const void *dy, co
     r.sums = a.sums;
     r.db = static_cast<__nv_bfloat16 *>(db);
     r.n = n;
-    return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");
+    return cuda_rc(launch_linear_reduce(r, true, s), "linear_reduce launch");
 }
 
 // partial [splits][n][k] = D_s^T X_s over the rows of split s, in fp32; with with_sums, also the column
 // sums of D per split. With one split dW and db themselves.
 int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long long rows, int k, int n, float *partial,
-                     float *sums, void *dw, void *db, bool with_sums, bool clear, const KernelCtl &ctl, const DevState &d,
-                     cudaStream_t s) {
+                     float *sums, void *dw, void *db, bool with_sums, bool clear, bool after, const KernelCtl &ctl,
+                     const DevState &d, cudaStream_t s) {
     LinearMaps m;
     if (int rc = map_operand(&m.a, D, n, (int)rows, true, 0)) return rc;
     if (int rc = map_operand(&m.b, X, k, (int)rows, true, 0)) return rc;
@@ -1417,10 +1419,11 @@ int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long l
     if (with_sums && direct) a.db_out = static_cast<__nv_bfloat16 *>(db);
     else if (with_sums) a.sums = sums;
     a.clear_status = clear ? 1 : 0;
+    a.more = !direct;
     a.ctl = ctl;
     const long long units = (long long)sp.splits * sp.tiles;
     const int grid = units < d.sms ? (int)units : d.sms;
-    return cuda_rc(launch_linear_tc(m, a, LIN_WG, 128, grid, s), "linear_tc launch");
+    return cuda_rc(launch_linear_tc(m, a, LIN_WG, 128, grid, after, s), "linear_tc launch");
 }
 
 }  // namespace
@@ -1800,7 +1803,7 @@ int trimul_linear_forward(const void *x, const void *residual, const trimul_line
     if ((rc = device_state(&d, true))) return rc;
     if ((rc = check_current_device({x, residual, y, p->weight, p->bias, p->workspace}, "linear pointer"))) return rc;
     return run_linear(LIN_FWD, x, p->weight, 0, residual, y, (int)p->rows, p->out_features, p->in_features, p->act,
-                      p->bias, nullptr, nullptr, true, linear_ctl(p), reinterpret_cast<cudaStream_t>(stream));
+                      p->bias, nullptr, nullptr, true, false, false, linear_ctl(p), reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t trimul_linear_backward_workspace_size(long long rows, int in_features, int out_features, int act, int from8) {
@@ -1843,12 +1846,14 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     uint8_t *base = static_cast<uint8_t *>(p->workspace);
     const KernelCtl ctl = linear_ctl(p);
     if ((dx || dw || db) && linear_one_pass(k, n)) return run_linear_one_pass(x, x8, dy, p, dx, dw, db, L, ctl, s);
-    bool clear = true;  // the call's first tensor kernel clears the status word
+    bool clear = true;   // the call's first tensor kernel clears the status word
+    bool after = false;  // a kernel of this call has been launched
     const bool d_pass = act != TRIMUL_ACT_NONE && (dx || dw || db);
     if (x8 && (dw || db || d_pass)) {
-        if ((rc = cuda_rc(launch_act8_unpack(codes, scales, base + L.x, rows * k, d->sms, s), "act8_unpack launch")))
+        if ((rc = cuda_rc(launch_act8_unpack(codes, scales, base + L.x, rows * k, d->sms, true, s), "act8_unpack launch")))
             return rc;
         x = base + L.x;
+        after = true;
     }
     float *sums = reinterpret_cast<float *>(base + L.sums), *partial = reinterpret_cast<float *>(base + L.partial);
     const LinearSplit sp = linear_split(rows, k, n);
@@ -1857,27 +1862,31 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     bool db_done = false;
     if (d_pass) {
         if ((rc = run_linear(LIN_GRAD, x, p->weight, 0, dy, base + L.d, (int)rows, n, k, act, p->bias,
-                             db ? sums : nullptr, db, clear, ctl, s)))
+                             db ? sums : nullptr, db, clear, after, dx || dw, ctl, s)))
             return rc;
         D = base + L.d;
         clear = false;
+        after = true;
         const int groups = linear_groups(rows, n);
         sum_rows = 4 * groups;
         db_done = groups == 1;
     }
     if (dx) {
         if ((rc = run_linear(LIN_FWD, D, p->weight, 1, nullptr, dx, (int)rows, k, n, TRIMUL_ACT_NONE, nullptr, nullptr,
-                             nullptr, clear, ctl, s)))
+                             nullptr, clear, after, dw || (db && !d_pass), ctl, s)))
             return rc;
         clear = false;
+        after = true;
     }
     // D is dy: its sums come with the weight product.
     const bool rows_sum = db && !d_pass;
     if (dw || rows_sum) {
         // One part is dW itself; where only db is wanted it goes to the workspace.
-        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, sums, dw ? dw : base + L.scrap, db, rows_sum, clear, ctl, *d, s)))
+        if ((rc = run_linear_wgrad(D, x, sp, rows, k, n, partial, sums, dw ? dw : base + L.scrap, db, rows_sum, clear, after,
+                                   ctl, *d, s)))
             return rc;
         clear = false;
+        after = true;
         if (sp.splits == 1) {
             dw = nullptr;
             db_done |= rows_sum;
@@ -1894,7 +1903,7 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
     r.db = db_done ? nullptr : static_cast<__nv_bfloat16 *>(db);
     r.n = n;
     r.sum_rows = sum_rows;
-    return cuda_rc(launch_linear_reduce(r, s), "linear_reduce launch");
+    return cuda_rc(launch_linear_reduce(r, after, s), "linear_reduce launch");
 }
 
 int trimul_linear_device_status(const trimul_linear_params *p, trimul_stream_t stream, int *detail) {
@@ -1931,7 +1940,7 @@ int trimul_act8_unpack(const void *codes, const void *scales, long long rows, in
     if ((rc = check_act8(x, rows, channels, codes, scales))) return rc;
     const DevState *d = nullptr;
     if ((rc = device_state(&d, true)) || (rc = check_current_device({x, codes, scales}, "act8 pointer"))) return rc;
-    return cuda_rc(launch_act8_unpack(codes, scales, x, rows * channels, d->sms, reinterpret_cast<cudaStream_t>(stream)),
+    return cuda_rc(launch_act8_unpack(codes, scales, x, rows * channels, d->sms, false, reinterpret_cast<cudaStream_t>(stream)),
                    "act8_unpack launch");
 }
 

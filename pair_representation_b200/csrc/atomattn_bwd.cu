@@ -517,8 +517,6 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-size_t atomattn_bwd_smem() { return ab::SMEM; }
-
 cudaError_t atomattn_bwd_setup() {
     return cudaFuncSetAttribute(atomattn_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ab::SMEM);
 }

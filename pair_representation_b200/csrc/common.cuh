@@ -178,6 +178,12 @@ static __device__ __noinline__ bool wait_bounded_cluster(uint64_t *bar, uint32_t
     }
 }
 
+// Kernels of one call that follow each other may overlap at their ends: a kernel lets the next one start
+// (its barriers, tensor memory and weights) as soon as SMs are free, and waits itself, before it reads or
+// writes what kernels before it in the call touch, until those are complete.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), no multicast
 // ---------------------------------------------------------------------------

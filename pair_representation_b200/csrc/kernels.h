@@ -309,6 +309,7 @@ struct LinearArgs {
     int out_bf16;           // LIN_WG, one split: Y is bf16
     __nv_bfloat16 *db_out;  // LIN_GRAD with one row-tile group (beside sums), LIN_WG with one split (instead): db itself
     int clear_status;
+    int more;  // a kernel of the same call comes next, and may start before this one is done
     KernelCtl ctl;
 };
 
@@ -330,10 +331,9 @@ struct LinearReduceArgs {
 };
 
 cudaError_t linear_tc_setup();
-// Whether a BN-wide slab of B with this many K blocks stays in shared memory.
-bool linear_resident(int bn, int kblocks);
-cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, cudaStream_t s);
-cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s);
+// after: a kernel of the same call comes before, and may still run when this one starts (it has `more`).
+cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, bool after, cudaStream_t s);
+cudaError_t launch_linear_reduce(LinearReduceArgs a, bool after, cudaStream_t s);
 
 // ---- the backward in one pass, in_features <= 128 (linear_bwd_tc.cu) ---------------
 
@@ -366,8 +366,8 @@ cudaError_t launch_linear_bwd(const LinearBwdMaps &m, const LinearBwdArgs &a, bo
 // ---- activations in 8 bits (act8.cu); values: a multiple of 32 -------------------
 
 cudaError_t launch_act8_pack(const void *x, void *codes, void *scales, long long values, int sms, cudaStream_t s);
-cudaError_t launch_act8_unpack(const void *codes, const void *scales, void *x, long long values, int sms,
-                               cudaStream_t s);
+cudaError_t launch_act8_unpack(const void *codes, const void *scales, void *x, long long values, int sms, bool more,
+                               cudaStream_t s);  // more: a kernel of the same call comes next
 
 // ---- static scratch of trimul_forward_noalloc (noalloc.cu) --------------------
 

@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     __syncthreads();
     if (kPair) cluster_sync();  // the peer's barriers are initialised
     tc_fence_after();
+    if (args.partial) next_kernel_may_start();  // the sums over the teams
     const uint32_t tmem = *tmem_slot;
     if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 

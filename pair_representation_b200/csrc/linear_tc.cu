@@ -265,6 +265,21 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    auto load_b = [&](uint8_t *dst, uint64_t *bar, int k0, int n0) {
+        if (!args.b_mn) {
+            tma_load_3d(dst, &tmB, bar, k0, n0, 0);
+        } else {
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h) tma_load_3d(dst + h * (BK * 128), &tmB, bar, n0 + 64 * h, k0, 0);
+        }
+    };
+    if (kResident && threadIdx.x == 0) {  // W: no kernel of the call writes it
+        const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
+        mbar_arrive_expect_tx(bfull, (uint32_t)(args.kblocks * B_BYTES));
+        for (int kb = 0; kb < args.kblocks; ++kb) load_b(bres + kb * B_BYTES, bfull, kb * BK, n0);
+    }
+    if (args.more) next_kernel_may_start();
+    wait_for_kernel_before();
     if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 
     if (warp == 0) {
@@ -274,19 +289,6 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            auto load_b = [&](uint8_t *dst, uint64_t *bar, int k0, int n0) {
-                if (!args.b_mn) {
-                    tma_load_3d(dst, &tmB, bar, k0, n0, 0);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < BN / 64; ++h) tma_load_3d(dst + h * (BK * 128), &tmB, bar, n0 + 64 * h, k0, 0);
-                }
-            };
-            if (kResident) {
-                const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
-                mbar_arrive_expect_tx(bfull, (uint32_t)(args.kblocks * B_BYTES));
-                for (int kb = 0; kb < args.kblocks; ++kb) load_b(bres + kb * B_BYTES, bfull, kb * BK, n0);
-            }
             Tiles<MODE> t(args);
             while (ok && t.next()) {
                 const int m0 = t.rt * BM, n0 = t.ct * BN;
@@ -554,6 +556,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) linear_reduce_kernel(const 
     __shared__ float4 part[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool weight = (int)blockIdx.x < a.weight_blocks;
+    wait_for_kernel_before();
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 s = zero, v[kReduceLoads];
     if (weight) {
@@ -597,12 +600,30 @@ __global__ void __launch_bounds__(kReduceWarps * 32) linear_reduce_kernel(const 
 
 }  // namespace
 
-cudaError_t launch_linear_reduce(LinearReduceArgs a, cudaStream_t s) {
+namespace {
+// A launch whose kernel may start while the one before it in the stream still runs (`after`).
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    Launch(int grid, int threads, size_t smem, bool after, cudaStream_t s) {
+        cfg.gridDim = dim3((unsigned)grid);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = after ? 1 : 0;
+    }
+};
+}  // namespace
+
+cudaError_t launch_linear_reduce(LinearReduceArgs a, bool after, cudaStream_t s) {
     a.weight_blocks = a.dw ? (int)((a.count / 4 + 31) / 32) : 0;
     const int grid = a.weight_blocks + (a.db ? (a.n + 31) / 32 : 0);
     if (grid == 0) return cudaSuccess;
-    linear_reduce_kernel<<<grid, kReduceWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    const Launch l(grid, kReduceWarps * 32, 0, after, s);
+    return cudaLaunchKernelEx(&l.cfg, linear_reduce_kernel, a);
 }
 
 namespace {
@@ -612,18 +633,19 @@ cudaError_t allow() {
                                 (int)lin::smem(BN, RES));
 }
 template <int BN, bool RES, int MODE>
-void go(const LinearMaps &m, const LinearArgs &a, int grid, cudaStream_t s) {
-    linear_tc_kernel<BN, RES, MODE><<<grid, lin::THREADS, lin::smem(BN, RES), s>>>(m.a, m.b, m.e, m.y, a);
+cudaError_t go(const LinearMaps &m, const LinearArgs &a, int grid, bool after, cudaStream_t s) {
+    const Launch l(grid, lin::THREADS, lin::smem(BN, RES), after, s);
+    return cudaLaunchKernelEx(&l.cfg, linear_tc_kernel<BN, RES, MODE>, m.a, m.b, m.e, m.y, a);
 }
 template <int MODE>
-void pick(const LinearMaps &m, const LinearArgs &a, int bn, bool res, int grid, cudaStream_t s) {
-    if (bn == 64) res ? go<64, true, MODE>(m, a, grid, s) : go<64, false, MODE>(m, a, grid, s);
-    else if (bn == 128) res ? go<128, true, MODE>(m, a, grid, s) : go<128, false, MODE>(m, a, grid, s);
-    else res ? go<256, true, MODE>(m, a, grid, s) : go<256, false, MODE>(m, a, grid, s);
+cudaError_t pick(const LinearMaps &m, const LinearArgs &a, int bn, int grid, bool after, cudaStream_t s) {
+    // Whether the slab of B stays in shared memory.
+    const bool res = (long long)a.kblocks * bn * lin::BK * 2 <= lin::RES_BYTES;
+    if (bn == 64) return res ? go<64, true, MODE>(m, a, grid, after, s) : go<64, false, MODE>(m, a, grid, after, s);
+    if (bn == 128) return res ? go<128, true, MODE>(m, a, grid, after, s) : go<128, false, MODE>(m, a, grid, after, s);
+    return res ? go<256, true, MODE>(m, a, grid, after, s) : go<256, false, MODE>(m, a, grid, after, s);
 }
 }  // namespace
-
-bool linear_resident(int bn, int kblocks) { return (long long)kblocks * bn * lin::BK * 2 <= lin::RES_BYTES; }
 
 cudaError_t linear_tc_setup() {
     cudaError_t e;
@@ -636,11 +658,9 @@ cudaError_t linear_tc_setup() {
     return allow<128, false, LIN_WG>();
 }
 
-cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, cudaStream_t s) {
-    if (mode == LIN_WG) go<128, false, LIN_WG>(m, a, grid, s);
-    else if (mode == LIN_GRAD) pick<LIN_GRAD>(m, a, bn, linear_resident(bn, a.kblocks), grid, s);
-    else pick<LIN_FWD>(m, a, bn, linear_resident(bn, a.kblocks), grid, s);
-    return cudaGetLastError();
+cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, bool after, cudaStream_t s) {
+    if (mode == LIN_WG) return go<128, false, LIN_WG>(m, a, grid, after, s);
+    return mode == LIN_GRAD ? pick<LIN_GRAD>(m, a, bn, grid, after, s) : pick<LIN_FWD>(m, a, bn, grid, after, s);
 }
 
 }  // namespace trimul
