@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     __syncthreads();
     if (kPair) cluster_sync();  // the peer's barriers are initialised
     tc_fence_after();
-    if (args.partial) next_kernel_may_start();  // the sums over the teams
     const uint32_t tmem = *tmem_slot;
     if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 
@@ -581,6 +580,9 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    // The sums over the teams. Here, not at the start: 147456 x 128 -> 128 with relu takes 36.0 us without the
+    // overlap, 35.4 so, and 37.1 with the sums' blocks waiting all the while.
+    if (args.partial) next_kernel_may_start();
     if (kPair) {
         cluster_sync();  // the counts of parts sent are here
         if (warp >= 2 && (h >> 1) == (int)rank && lane == 0) {
