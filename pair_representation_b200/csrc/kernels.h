@@ -327,7 +327,7 @@ struct LinearReduceArgs {
     const float *sums;
     __nv_bfloat16 *db;
     int n, sum_rows;
-    int weight_blocks;  // set by the launcher
+    int weight_blocks, join;  // set by the launcher: blocks of dw, warps that share their places
 };
 
 cudaError_t linear_tc_setup();

@@ -536,10 +536,11 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // Sums of the split products and of the column-sum partials, rounded once to bf16.
-// dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. A block takes 32 places; its
-// sixteen warps each add every sixteenth partial (at most ten, all in flight at once), and
-// the sixteen sums are joined in shared memory in order: the result does not depend on
-// the launch. Up to 148 partials, bound by the latency of reading them.
+// dw[i] = sum_s partial[s][i]; db[j] = sum_s sums[s][j]. A warp takes 32 places and at most
+// ten partials of them at a time, all in flight at once: up to ten partials need one warp, up to
+// 148 a block's sixteen, whose sums are joined in shared memory in order: the result does not
+// depend on the launch. Bound by the latency of reading the partials where there are many, by
+// their bytes where there are few.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -556,28 +557,30 @@ __global__ void __launch_bounds__(kReduceWarps * 32) linear_reduce_kernel(const 
     __shared__ float4 part[kReduceWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool weight = (int)blockIdx.x < a.weight_blocks;
+    // `join` warps share their places, each with every join-th partial.
+    const int join = weight ? a.join : kReduceWarps, first = warp & (join - 1);
+    const long long i = ((long long)blockIdx.x * (kReduceWarps / join) + warp / join) * 32 + lane;  // four values of dw
+    const long long quads = a.count >> 2;  // n k is a multiple of 64
+    const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
     wait_for_kernel_before();
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     float4 s = zero, v[kReduceLoads];
     if (weight) {
-        const long long quads = a.count >> 2;  // n k is a multiple of 64
-        const long long i = (long long)blockIdx.x * 32 + lane;
         const float4 *p = reinterpret_cast<const float4 *>(a.partial) + i;
-        for (int k0 = warp; k0 < a.splits; k0 += kReduceWarps * kReduceLoads) {
+        for (int k0 = first; k0 < a.splits; k0 += join * kReduceLoads) {
 #pragma unroll
             for (int u = 0; u < kReduceLoads; ++u) {
-                const int k = k0 + u * kReduceWarps;
+                const int k = k0 + u * join;
                 v[u] = i < quads && k < a.splits ? __ldcs(p + (size_t)k * quads) : zero;
             }
 #pragma unroll
             for (int u = 0; u < kReduceLoads; ++u) add4(s, v[u]);
         }
     } else {
-        const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
-        for (int k0 = warp; k0 < a.sum_rows; k0 += kReduceWarps * kReduceLoads) {
+        for (int k0 = first; k0 < a.sum_rows; k0 += join * kReduceLoads) {
 #pragma unroll
             for (int u = 0; u < kReduceLoads; ++u) {
-                const int k = k0 + u * kReduceWarps;
+                const int k = k0 + u * join;
                 v[u].x = j < a.n && k < a.sum_rows ? a.sums[(size_t)k * a.n + j] : 0.f;
             }
 #pragma unroll
@@ -586,14 +589,11 @@ __global__ void __launch_bounds__(kReduceWarps * 32) linear_reduce_kernel(const 
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int k = 1; k < kReduceWarps; ++k) add4(s, part[k][lane]);
+    if (first != 0) return;
+    for (int k = 1; k < join; ++k) add4(s, part[warp + k][lane]);
     if (weight) {
-        const long long i = (long long)blockIdx.x * 32 + lane;
-        if (i < a.count >> 2) reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+        if (i < quads) reinterpret_cast<uint2 *>(a.dw)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
     } else {
-        const int j = ((int)blockIdx.x - a.weight_blocks) * 32 + lane;
         if (j < a.n) a.db[j] = __float2bfloat16_rn(s.x);
     }
 }
@@ -619,7 +619,10 @@ struct Launch {
 }  // namespace
 
 cudaError_t launch_linear_reduce(LinearReduceArgs a, bool after, cudaStream_t s) {
-    a.weight_blocks = a.dw ? (int)((a.count / 4 + 31) / 32) : 0;
+    a.join = 1;
+    while (a.join < kReduceWarps && a.join * kReduceLoads < a.splits) a.join *= 2;
+    const long long places = 32 * (kReduceWarps / a.join);  // of a block, four values each
+    a.weight_blocks = a.dw ? (int)((a.count / 4 + places - 1) / places) : 0;
     const int grid = a.weight_blocks + (a.db ? (a.n + 31) / 32 : 0);
     if (grid == 0) return cudaSuccess;
     const Launch l(grid, kReduceWarps * 32, 0, after, s);
