@@ -23,6 +23,10 @@
 // swizzled tile without conflicts, and a lane's part of db is eight columns: it adds its rows in
 // registers, tile after tile, and the lanes are joined once, at the end.
 //
+// Measured: 147456 x 128 -> 128 with sigmoid 33 us, of which the sums over the CTAs are 4 and the start,
+// where every CTA waits for its first tiles at once, 5; -> 512 with silu 111 us, x in 8 bits 126 us:
+// there the workers wait, on tensor memory and for their pair's part of dx.
+//
 // Roles: warp 0 TMA, warp 1 MMA issue, warps 2-17 workers. Every wait is bounded; see the barrier
 // list below. Order within a tile, so that no role waits on itself: the MMA warp issues p of
 // the next unit before it waits for D of this one (kHeld8: not across tiles, where x is still read),
