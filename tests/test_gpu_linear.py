@@ -320,3 +320,22 @@ def test_relu_sign_under_a_large_bias(k, n):
     ref = np.where(p > 0, dy, 0).sum(axis=0)
     assert np.abs(ref).max() <= 256
     assert np.array_equal(db.double().cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("rows", [1, 300, 3000])
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("held", [False, True])
+def test_parts_of_the_backward_in_several_products(rows, act, held):
+    """Each choice of gradients, where every one is a product of its own: those of the whole call, bit for bit.
+    (With act none, db comes with dW's product, whose own result may not be wanted.)"""
+    x, w, b, dy = (dev(t) for t in draw(rows, 160, 200, 13))
+    xx = tm.act8_pack(x) if held else x
+    whole = tm.linear_backward(xx, w, dy, bias=b, act=act)
+    for i in range(7):
+        need = [bool(i & 1 << j) for j in range(3)]
+        ws = torch.zeros(tm.trimul_linear_backward_workspace_size(rows, 160, 200, tm.ACTS[act], held), dtype=torch.uint8,
+                         device=DEV)
+        part = tm.linear_backward(xx, w, dy, b, act, *need, workspace=ws)
+        assert tm.device_status(ws)[0] == 0
+        for want, p, q in zip(need, part, whole):
+            assert (p is not None) == want and (p is None or torch.equal(p, q))
