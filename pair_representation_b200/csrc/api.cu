@@ -1215,9 +1215,21 @@ int linear_teams(long long rows, int n) {
     return tiles < most ? tiles : most;
 }
 
+// Height of LIN_FWD's row tiles in units of 128: two where B is streamed beside A, so that B's blocks serve
+// twice the rows and more of A is in flight (147456 x 512 -> 128 39 -> 36 us, -> 384 89 -> 70); unless SMs
+// would be without a tile, or the last round of tiles leaves more than an eighth of the time unused (40000 x
+// 512 -> 128 with silu 16.6 -> 18.7). LIN_GRAD, bound by its drain, gains nothing (512 -> 128 with silu: 128
+// -> 131 us).
+int linear_high(long long M, int N, int K) {
+    const int bn = linear_bn(M, N), cols = ceil_div(N, bn), groups = kLinearCtas / cols;
+    const int tall = ceil_div(M, 256), low = ceil_div(M, 128);
+    const bool streamed = bn <= 128 && !linear_resident(bn, ceil_div(K, 64));
+    return streamed && (long long)tall * cols >= kLinearCtas && 16ll * ceil_div(tall, groups) <= 9ll * ceil_div(low, groups) ? 2 : 1;
+}
+
 // The groups of CTAs that take row tiles in turn in a product of M x N (LIN_FWD, LIN_GRAD).
-int linear_groups(long long M, int N) {
-    const int tiles = ceil_div(M, 128), groups = kLinearCtas / ceil_div(N, linear_bn(M, N));
+int linear_groups(long long M, int N, int high) {
+    const int tiles = ceil_div(M, 128 * high), groups = kLinearCtas / ceil_div(N, linear_bn(M, N));
     return groups < tiles ? groups : tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
 }
 
@@ -1246,7 +1258,7 @@ LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int fro
         const LinearSplit s = linear_split(rows, k, n);
         if (s.splits > 1) L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
         // Column sums of D: four per row-tile group of the D product, or one row per part of dW.
-        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * linear_groups(rows, n) : s.splits > 1 ? (size_t)s.splits : 0;
+        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * linear_groups(rows, n, 1) : s.splits > 1 ? (size_t)s.splits : 0;
         L.sums = take(sums * n * 4);
         // dW where only db is wanted and its sums come with the product.
         L.scrap = take(s.splits == 1 && act == TRIMUL_ACT_NONE ? (size_t)n * k * 2 : 0);
@@ -1296,7 +1308,7 @@ int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
 }
 
 // Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. LIN_GRAD: sums has four rows for each
-// of linear_groups(M, N), or where there is one group db itself is written too.
+// of linear_groups(M, N, 1), or where there is one group db itself is written too.
 int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, void *Y, int M, int N, int K, int act,
                const void *bias, float *sums, void *db, bool clear, bool after, bool more, const KernelCtl &ctl,
                cudaStream_t s) {
@@ -1313,10 +1325,11 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.M = M;
     a.N = N;
     a.b_mn = b_mn;
-    a.row_tiles = ceil_div(M, 128);
+    a.high = mode == LIN_FWD ? linear_high(M, N, K) : 1;
+    a.row_tiles = ceil_div(M, 128 * a.high);
     a.col_tiles = ceil_div(N, bn);
     a.kblocks = ceil_div(K, 64);
-    a.groups = linear_groups(M, N);
+    a.groups = linear_groups(M, N, a.high);
     a.splits = 1;
     a.kb_per_split = a.kblocks;
     a.act = act;
@@ -1412,6 +1425,7 @@ int run_linear_wgrad(const void *D, const void *X, const LinearSplit &sp, long l
     memset(&a, 0, sizeof a);
     a.M = n;
     a.N = k;
+    a.high = 1;
     a.a_mn = a.b_mn = 1;
     a.row_tiles = ceil_div(n, 128);
     a.col_tiles = ceil_div(k, 128);
@@ -1870,7 +1884,7 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
         D = base + L.d;
         clear = false;
         after = true;
-        const int groups = linear_groups(rows, n);
+        const int groups = linear_groups(rows, n, 1);
         sum_rows = 4 * groups;
         db_done = groups == 1;
     }

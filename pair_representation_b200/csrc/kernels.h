@@ -297,6 +297,7 @@ enum LinearAct { LIN_NONE = 0, LIN_RELU = 1, LIN_SIGMOID = 2, LIN_SILU = 3 };  /
 struct LinearArgs {
     int M, N;                  // rows and columns of Y
     int a_mn, b_mn;            // operand stored [k][rows] instead of [rows][k]
+    int high;                  // LIN_FWD: row tiles of 128, or (2) of 256
     int row_tiles, col_tiles, kblocks;
     int groups;                // LIN_FWD, LIN_GRAD: CTA c owns column tile c % col_tiles and the row tiles
                                // c / col_tiles, + groups, ...
@@ -331,6 +332,8 @@ struct LinearReduceArgs {
 };
 
 cudaError_t linear_tc_setup();
+// Whether a BN-wide slab of B with this many K blocks stays in shared memory.
+bool linear_resident(int bn, int kblocks);
 // after: a kernel of the same call comes before, and may still run when this one starts (it has `more`).
 cudaError_t launch_linear_tc(const LinearMaps &m, const LinearArgs &a, int mode, int bn, int grid, bool after, cudaStream_t s);
 cudaError_t launch_linear_reduce(LinearReduceArgs a, bool after, cudaStream_t s);

@@ -45,13 +45,17 @@ constexpr int RES_BYTES = 65536;            // resident slab of B
 constexpr int TMEM_COLS = 512;
 constexpr int ONES_COL = 256;               // LIN_WG (BN = 128): accumulators of the ones column
 
-__host__ __device__ constexpr int stages(int bn, bool res) { return res ? 5 : bn == 256 ? 3 : 4; }
-__host__ __device__ constexpr int stage_bytes(int bn, bool res) { return A_BYTES + (res ? 0 : bn * BK * 2); }
-__host__ __device__ constexpr size_t smem(int bn, bool res) {
-    return 1024 + (size_t)stages(bn, res) * stage_bytes(bn, res) + (res ? RES_BYTES : 0) + OUT_BYTES + BIAS_BYTES +
+__host__ __device__ constexpr int stages(int bn, bool res, int high = 1) { return res ? 5 : bn == 256 || high == 2 ? 3 : 4; }
+__host__ __device__ constexpr int stage_bytes(int bn, bool res, int high = 1) {
+    return high * A_BYTES + (res ? 0 : bn * BK * 2);
+}
+__host__ __device__ constexpr size_t smem(int bn, bool res, int high = 1) {
+    return 1024 + (size_t)stages(bn, res, high) * stage_bytes(bn, res, high) + (res ? RES_BYTES : 0) + OUT_BYTES + BIAS_BYTES +
            ONES_BYTES + BAR_BYTES;
 }
-static_assert(smem(256, false) <= 232448 && smem(256, true) <= 232448 && smem(128, false) <= 232448, "shared memory");
+static_assert(smem(256, false) <= 232448 && smem(256, true) <= 232448 && smem(128, false) <= 232448 &&
+                  smem(128, false, 2) <= 232448,
+              "shared memory");
 
 // The tiles of one CTA, in the order every role of the CTA visits them.
 template <int MODE>
@@ -205,16 +209,19 @@ __device__ __forceinline__ float column_sum32(const float2 *v, int lane) {
 
 }  // namespace
 
-template <int BN, bool kResident, int MODE>
+template <int BN, bool kResident, int MODE, int HIGH>
 __global__ void __launch_bounds__(lin::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmY,
                      const LinearArgs args) {
     using namespace lin;
-    constexpr int STAGES = stages(BN, kResident), STAGE_BYTES = stage_bytes(BN, kResident);
+    static_assert(HIGH == 1 || (BN <= 128 && MODE == LIN_FWD), "a drain warp's chunks are then of the same columns");
+    constexpr int STAGES = stages(BN, kResident, HIGH), STAGE_BYTES = stage_bytes(BN, kResident, HIGH);
     constexpr int B_BYTES = BN * BK * 2;
     constexpr int CHUNK = 32;                                      // accumulator columns per stored block
-    constexpr int CHUNKS = BN / CHUNK, MINE = (CHUNKS + 3) / 4;  // of a tile, and of them a drain warp's (at most)
+    constexpr int WIDE = BN / CHUNK;                               // of a row of the tile
+    constexpr int CHUNKS = HIGH * WIDE, MINE = (CHUNKS + 3) / 4;  // of a tile, and of them a drain warp's (at most)
+    constexpr int COLS = (WIDE + 3) / 4;                           // a drain warp's chunks of a row
     constexpr int BLOCK = MODE == LIN_WG ? 4096 : 2048, BUFS = WBUF / BLOCK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -295,7 +302,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
             bool ok = true;
             Tiles<MODE> t(args);
             while (ok && t.next()) {
-                const int m0 = t.rt * BM, n0 = t.ct * BN;
+                const int m0 = t.rt * (HIGH * BM), n0 = t.ct * BN;
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl, SITE_LIN | 2, t.rt)) {
                         ok = false;
@@ -305,12 +312,13 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
                     const int k0 = kb * BK;
                     if (!args.a_mn) {
-                        tma_load_3d(sa, &tmA, &full[stage], k0, m0, 0);
+#pragma unroll
+                        for (int r = 0; r < HIGH; ++r) tma_load_3d(sa + r * A_BYTES, &tmA, &full[stage], k0, m0 + r * BM, 0);
                     } else {
                         tma_load_3d(sa, &tmA, &full[stage], m0, k0, 0);
                         tma_load_3d(sa + BK * 128, &tmA, &full[stage], m0 + 64, k0, 0);
                     }
-                    if (!kResident) load_b(sa + A_BYTES, &full[stage], k0, n0);
+                    if (!kResident) load_b(sa + HIGH * A_BYTES, &full[stage], k0, n0);
                     ++issued;
                     if (++stage == STAGES) {
                         stage = 0;
@@ -341,7 +349,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * BN);
+                const uint32_t d = tmem + (uint32_t)(acc * HIGH * BN);
                 const bool sum_rows = with_ones && t.ct == 0;
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
                     if (!wait_bounded(&full[stage], phase, abort_flag, ctl, SITE_LIN | 5, t.rt)) {
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(ring + stage * STAGE_BYTES);
-                    const uint32_t sb = kResident ? smem_u32(bres + kb * B_BYTES) : sa + A_BYTES;
+                    const uint32_t sb = kResident ? smem_u32(bres + kb * B_BYTES) : sa + HIGH * A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk) {
                         const uint64_t ad = args.a_mn ? sdesc_sw128(sa + kk * 2048, BK * 128, 1024)
@@ -359,6 +367,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                                                       : sdesc_sw128(sb + kk * 32, 16, 1024);
                         const uint32_t more = (kb != t.kb0 || kk != 0) ? 1u : 0u;
                         mma_bf16(d, ad, bd, idesc, more);
+                        if (HIGH == 2)
+                            mma_bf16(d + BN, sdesc_sw128(sa + A_BYTES + kk * 32, 16, 1024), bd, idesc, more);
                         if (sum_rows)
                             mma_bf16(tmem + ONES_COL + 16 * acc, ad, sdesc_sw128(smem_u32(ones) + kk * 32, 16, 1024),
                                      idesc_ones, more);
@@ -378,15 +388,15 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         }
     } else {
         // ---------------- drain warps 2..17 ----------------
-        // Warp (q, h): accumulator rows 32 q .. 32 q + 31, chunks h and h + 4 of each tile. Block n of
-        // this warp (counted over all its tiles) goes through buffer n % BUFS.
+        // Warp (q, h): accumulator rows 32 q .. 32 q + 31, chunks h and h + 4 of each tile (HIGH = 2: the
+        // second of them the same columns of the lower 128 rows). Block n of this warp (counted over all its tiles) goes through buffer n % BUFS.
         const int ew = warp - 2, q = warp & 3, h = ew >> 2;
         uint8_t *wbuf = outbuf + ew * WBUF;
         uint64_t *ebar = efull + 2 * ew;
         float *mybias = biasbuf + ew * 64;
         const uint32_t lanebase = tmem + ((uint32_t)(q * 32) << 16);
         const bool has_e = MODE != LIN_WG && args.has_e;
-        float colsum[MINE];
+        float colsum[COLS];
         int nst = 0, nload = 0, lt = 0;
 
         // Iterator over this warp's blocks, for the E loads that run one block ahead.
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     ahead_c = h;
                     if (ahead_c >= CHUNKS) continue;
                 }
-                const int col = ahead.ct * BN + ahead_c * CHUNK, row = ahead.rt * BM + 32 * q;
+                const int col = ahead.ct * BN + ahead_c % WIDE * CHUNK, row = (ahead.rt * HIGH + ahead_c / WIDE) * BM + 32 * q;
                 if (col < args.N && row < args.M) {
                     if (lane == 0) {
                         tma_store_wait_read<0>();  // the block that last left from this buffer has been read
@@ -421,27 +431,28 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         if (MODE != LIN_WG) {
             const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
 #pragma unroll
-            for (int i = 0; i < MINE; ++i) {
-                const int col = n0 + (h + 4 * i) * 32 + lane;
+            for (int i = 0; i < COLS; ++i) {
+                const int col = n0 + (HIGH == 2 ? h % WIDE : h + 4 * i) * 32 + lane;
                 mybias[32 * i + lane] = (args.bias && col < args.N) ? __bfloat162float(args.bias[col]) : 0.f;
             }
             __syncwarp();
         }
 #pragma unroll
-        for (int i = 0; i < MINE; ++i) colsum[i] = 0.f;
+        for (int i = 0; i < COLS; ++i) colsum[i] = 0.f;
         bool ok = true;
         Tiles<MODE> t(args);
         while (ok && t.next()) {
             const int acc = lt & 1;
             if (!warp_wait(&tfull[acc], (uint32_t)(lt >> 1) & 1u, abort_flag, ctl, SITE_LIN | 6, t.rt)) break;
             tc_fence_after();
-            const int row0 = t.rt * BM + 32 * q;
+            const int top = t.rt * (HIGH * BM) + 32 * q;
 #pragma unroll
             for (int ci = 0; ci < MINE; ++ci) {
-                const int ch = h + 4 * ci, col = t.ct * BN + ch * CHUNK;
+                const int ch = h + 4 * ci, wide = HIGH == 2 ? ch % WIDE : ch, col = t.ct * BN + wide * CHUNK;
+                const int row0 = top + (HIGH == 2 ? ch / WIDE * BM : 0), mine = HIGH == 2 ? 0 : ci;
                 if (ch >= CHUNKS || row0 >= args.M || col >= args.N) continue;
                 uint8_t *ob = wbuf + (nst % BUFS) * BLOCK;
-                const uint32_t taddr = lanebase + (uint32_t)(acc * BN + ch * CHUNK);
+                const uint32_t taddr = lanebase + (uint32_t)(acc * HIGH * BN + ch * CHUNK);
                 uint32_t v[32];
                 tmem_ld32(taddr, v);
                 if (has_e) {
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                                 make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                     }
                 } else {
-                    const float *bias = mybias + 32 * ci;
+                    const float *bias = mybias + 32 * mine;
                     float2 p[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                         finish<MODE, true>(args.act, p, row, swz);
                     else
                         finish<MODE, false>(args.act, p, row, swz);
-                    if (MODE == LIN_GRAD && args.sums != nullptr) colsum[ci] += column_sum32(p, lane);
+                    if (MODE == LIN_GRAD && args.sums != nullptr) colsum[mine] += column_sum32(p, lane);
                 }
                 ++nst;
                 fence_proxy_async_smem();
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                 uint32_t v[16];
                 tmem_ld16(lanebase + (uint32_t)(ONES_COL + 16 * acc), v);
                 tmem_ld_wait_regs(v);
-                const int row = row0 + lane;
+                const int row = top + lane;
                 if (row < args.M) {
                     if (args.db_out) args.db_out[row] = __float2bfloat16_rn(__uint_as_float(v[0]));
                     else args.sums[(size_t)t.split * args.M + row] = __uint_as_float(v[0]);
@@ -514,9 +525,9 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         if (MODE == LIN_GRAD && args.sums != nullptr) {
             float *dst = args.sums + (size_t)(((int)blockIdx.x / args.col_tiles) * 4 + q) * args.N;
 #pragma unroll
-            for (int i = 0; i < MINE; ++i) {
+            for (int i = 0; i < COLS; ++i) {
                 const int ch = h + 4 * i, col = ((int)blockIdx.x % args.col_tiles) * BN + ch * 32 + lane;
-                if (ch < CHUNKS && col < args.N) dst[col] = colsum[i];
+                if (ch < WIDE && col < args.N) dst[col] = colsum[i];
             }
         }
         // E blocks still in flight (only after a timeout: a complete pass consumed them all).
@@ -633,21 +644,24 @@ cudaError_t launch_linear_reduce(LinearReduceArgs a, bool after, cudaStream_t s)
     return cudaLaunchKernelEx(&l.cfg, linear_reduce_kernel, a);
 }
 
+bool linear_resident(int bn, int kblocks) { return (long long)kblocks * bn * lin::BK * 2 <= lin::RES_BYTES; }
+
 namespace {
-template <int BN, bool RES, int MODE>
+template <int BN, bool RES, int MODE, int HIGH = 1>
 cudaError_t allow() {
-    return cudaFuncSetAttribute(linear_tc_kernel<BN, RES, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)lin::smem(BN, RES));
+    return cudaFuncSetAttribute(linear_tc_kernel<BN, RES, MODE, HIGH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)lin::smem(BN, RES, HIGH));
 }
-template <int BN, bool RES, int MODE>
+template <int BN, bool RES, int MODE, int HIGH = 1>
 cudaError_t go(const LinearMaps &m, const LinearArgs &a, int grid, bool after, cudaStream_t s) {
-    const Launch l(grid, lin::THREADS, lin::smem(BN, RES), after, s);
-    return cudaLaunchKernelEx(&l.cfg, linear_tc_kernel<BN, RES, MODE>, m.a, m.b, m.e, m.y, a);
+    const Launch l(grid, lin::THREADS, lin::smem(BN, RES, HIGH), after, s);
+    return cudaLaunchKernelEx(&l.cfg, linear_tc_kernel<BN, RES, MODE, HIGH>, m.a, m.b, m.e, m.y, a);
 }
 template <int MODE>
 cudaError_t pick(const LinearMaps &m, const LinearArgs &a, int bn, int grid, bool after, cudaStream_t s) {
-    // Whether the slab of B stays in shared memory.
-    const bool res = (long long)a.kblocks * bn * lin::BK * 2 <= lin::RES_BYTES;
+    const bool res = linear_resident(bn, a.kblocks);
+    if (MODE == LIN_FWD && a.high == 2)
+        return bn == 64 ? go<64, false, LIN_FWD, 2>(m, a, grid, after, s) : go<128, false, LIN_FWD, 2>(m, a, grid, after, s);
     if (bn == 64) return res ? go<64, true, MODE>(m, a, grid, after, s) : go<64, false, MODE>(m, a, grid, after, s);
     if (bn == 128) return res ? go<128, true, MODE>(m, a, grid, after, s) : go<128, false, MODE>(m, a, grid, after, s);
     return res ? go<256, true, MODE>(m, a, grid, after, s) : go<256, false, MODE>(m, a, grid, after, s);
@@ -660,7 +674,7 @@ cudaError_t linear_tc_setup() {
         (e = allow<128, false, LIN_FWD>()) || (e = allow<256, true, LIN_FWD>()) || (e = allow<256, false, LIN_FWD>()) ||
         (e = allow<64, true, LIN_GRAD>()) || (e = allow<64, false, LIN_GRAD>()) || (e = allow<128, true, LIN_GRAD>()) ||
         (e = allow<128, false, LIN_GRAD>()) || (e = allow<256, true, LIN_GRAD>()) ||
-        (e = allow<256, false, LIN_GRAD>()))
+        (e = allow<256, false, LIN_GRAD>()) || (e = allow<64, false, LIN_FWD, 2>()) || (e = allow<128, false, LIN_FWD, 2>()))
         return e;
     return allow<128, false, LIN_WG>();
 }

@@ -339,3 +339,13 @@ def test_parts_of_the_backward_in_several_products(rows, act, held):
         assert tm.device_status(ws)[0] == 0
         for want, p, q in zip(need, part, whole):
             assert (p is not None) == want and (p is None or torch.equal(p, q))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("rows,k,n", [(37800, 264, 72), (60001, 320, 72), (37800, 72, 520), (19000, 320, 360), (37800, 560, 40),
+                                      (60001, 520, 64)])
+def test_tall_tiles(rows, k, n, act):
+    """Contractions too long for W to stay on chip, over rows enough for tiles of 256: a last one that is cut,
+    several rounds of them, several column tiles."""
+    check_forward(rows, k, n, act, True, act != "relu")
+    check_backward(rows, k, n, act)
