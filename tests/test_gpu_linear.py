@@ -349,3 +349,37 @@ def test_tall_tiles(rows, k, n, act):
     several rounds of them, several column tiles."""
     check_forward(rows, k, n, act, True, act != "relu")
     check_backward(rows, k, n, act)
+
+
+@pytest.mark.parametrize("n", [8, 64, 72, 128, 256, 264, 384, 512])
+@pytest.mark.parametrize("rows", [100, 20000, 60001])
+def test_every_length_of_the_contraction(rows, n):
+    """1 to 17 blocks of 64: each place in the ring where a tile may end, with W on chip and streamed, tiles of 128 and
+    256 rows. Whole numbers small enough that every sum, the bias with it, is exact in fp32: one rounding."""
+    gen = torch.Generator(device=DEV).manual_seed(rows + n)
+    whole = lambda *s: torch.randint(-4, 5, s, generator=gen, device=DEV).to(torch.bfloat16)  # noqa: E731
+    b = torch.arange(n, device=DEV).remainder(97).to(torch.bfloat16)
+    for blocks in range(1, 18):
+        x, w = whole(rows, 64 * blocks), whole(n, 64 * blocks)
+        # 1088 products of at most 16 and the bias: under 2^15, exact in fp32 in any order
+        ref = torch.nn.functional.linear(x.double(), w.double(), b.double())
+        assert torch.equal(tm.linear(x, w, b), ref.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("k,n", [(160, 72), (128, 128), (96, 256), (128, 512), (320, 384), (72, 520)])
+def test_backward_over_every_number_of_row_blocks(k, n):
+    """1 to 20 blocks of 64 rows, and 1 to 4 tiles for each CTA of the form in one pass, all sums exact in fp32 (whole
+    numbers up to 4: at most 76001 products of 16, under 2^24): one rounding. relu with a bias that makes p no whole
+    number, so that no sign is in doubt."""
+    gen = torch.Generator(device=DEV).manual_seed(k + n)
+    whole = lambda *s: torch.randint(-4, 5, s, generator=gen, device=DEV).to(torch.bfloat16)  # noqa: E731
+    w, b = whole(n, k), torch.full((n,), 0.5, device=DEV, dtype=torch.bfloat16)
+    for rows in [64 * i - i % 3 for i in range(1, 21)] + [19000, 38000, 57000, 76001]:
+        x, dy = whole(rows, k), whole(rows, n)
+        for act in ("none", "relu"):
+            D = dy.double()
+            if act == "relu":
+                D = D * (x.double() @ w.double().T + 0.5 > 0)
+            ref = (D @ w.double(), D.T @ x.double(), D.sum(0))
+            for got, want in zip(tm.linear_backward(x, w, dy, b, act), ref):
+                assert torch.equal(got, want.to(torch.bfloat16)), (rows, act)
