@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                 if (clear) tmem_zero32(mytmem + (x ? DV_COL : DK_COL));
                 const float f = x ? 1.f : scale;
                 // Through P's tile, which is free from the window's sums to the next window's P: a lane's 64 bytes
-                // straight to memory are 32 rows an instruction, and such stores were a quarter of the
-                // passes through L1's data pipe (157 -> 148 us without them). (A block that starts before the first atom: there is
-                // one for each sequence.)
+                // straight to memory are 32 rows an instruction, and such stores were a quarter of the passes
+                // through L1's data pipe (157 -> 148 us without them). (A block that starts before the first
+                // atom: there is one for each sequence.)
                 uint8_t *tile = (x ? dv_tile : smem + OFF_P + warp * TILE) + lane * 64;
                 __nv_bfloat16 *dst = (x ? args.dv : args.dk) + ((size_t)b * n + atom) * row_elems + h * 32;
 #pragma unroll

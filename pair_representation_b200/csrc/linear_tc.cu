@@ -25,7 +25,8 @@
 //
 // Measured: 147456 x 512 -> 128 with a residual 40 us (5.7 TB/s); 589824 x 128 -> 512 137 us
 // (5.5 TB/s), with silu 163 us at 1965 MHz (190 at the 1650 MHz that the power cap leaves in long runs):
-// the drain warps then issue at 54 % of their slots and wait on exponentials and shared memory. Sixteen warps on blocks of 32 columns (eight on 64 columns: 188 us).
+// the drain warps then issue at 54 % of their slots and wait on exponentials and shared memory.
+// Sixteen warps on blocks of 32 columns (eight on 64 columns: 188 us).
 //
 // Every wait is bounded; on a timeout the CTA lets its copies land and returns.
 #include "kernels.h"
