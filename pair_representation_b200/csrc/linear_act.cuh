@@ -72,10 +72,11 @@ __device__ __forceinline__ float act_fwd(float p) {
 }
 
 // act'(p) d. 1 - s is taken as s exp(-p), which keeps its digits where s is next to 1. p stops at
-// -87, where both factors are still finite and every slope is under 2e-36.
+// -88: exp(-p) is finite there, and s, under the smallest normal number, is 0, and with it the slope, of
+// -infinity too.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float p, float d) {
-    p = max_nan(p, -87.f);
+    p = max_nan(p, -88.f);
     const float e = ex2f(p * -1.4426950408889634f), s = rcpf(1.f + e), c = s * e;
     return ACT == LIN_SIGMOID ? d * (s * c) : d * fmaf(p * s, c, s);
 }
