@@ -462,8 +462,16 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             // One test for all of the warp's values: the four blocks below then overlap, and their matrix loads
             // and stores, which the whole warp does together, stand on one side of the branch.
             const bool share = !has_p || ACT == LIN_RELU || __all_sync(0xffffffffu, can_share(p));
-            if (!share) write_d<ACT, false>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
-            else write_d<ACT, true>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
+            if (!share) {
+                // Places outside the matrices are products with zeros, NaN where one met an infinity (and a NaN is never
+                // shared): p is 0 there, so that with dy = 0 (TMA's fill) D is 0 too. (relu's D is 0 where p is not over 0.)
+                const int cols_left = n_mine - (c * 128 + 32 * h), rows_left = (int)args.rows - (row0(t) + 32 * q);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (8 * ((i >> 1) & 3) >= cols_left || 16 * (i >> 3) + 8 * (i & 1) + (lane >> 2) >= rows_left)
+                        p[i] = make_float2(0.f, 0.f);
+                write_d<ACT, false>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
+            } else write_d<ACT, true>(p, keep, tile, 4 * (h & 1) + la_c, x7, dsum);
 #pragma unroll
             for (int cc = 0; cc < CHUNKS; ++cc)
                 if (cc == c)

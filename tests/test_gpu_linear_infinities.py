@@ -71,3 +71,28 @@ def test_slope_at_minus_infinity(k, n):
     b[:] = -np.inf
     dx, dw, db = tm.linear_backward(dev(x), dev(w), dev(dy), bias=dev(b), act="sigmoid")
     assert all((t == 0).all() for t in (dx, dw, db))
+
+
+# One pass (one column chunk, two, pairs) with columns past out_features, and the several products.
+SIZES = [(128, 72), (64, 128), (128, 200), (40, 256), (96, 392), (160, 72), (264, 136)]
+
+
+@pytest.mark.parametrize("rows", [100, 128, 20000])
+@pytest.mark.parametrize("k,n", SIZES)
+def test_infinity_in_a_row_of_x(rows, k, n):
+    """Every p of the row is infinite and sigmoid's slope there 0: dx of the row is 0."""
+    x, w, b, dy = draw(rows, k, n, 1)
+    x[rows // 2, 3] = np.inf
+    x[rows - 1, 5] = -np.inf
+    assert (w[:, [3, 5]] != 0).all()
+    check(x, w, b, dy, "sigmoid")
+
+
+@pytest.mark.parametrize("rows", [100, 128, 20000 + 64])
+@pytest.mark.parametrize("k,n", SIZES[:5])
+def test_infinity_in_a_row_of_w(rows, k, n):
+    """Every p of one column is infinite: its row of dW and its place in db are 0, whatever the number of rows."""
+    x, w, b, dy = draw(rows, k, n, 2)
+    w[n // 2, 3], w[n - 1, 5] = np.inf, -np.inf
+    assert (x[:, [3, 5]] != 0).all()
+    check(x, w, b, dy, "sigmoid")
