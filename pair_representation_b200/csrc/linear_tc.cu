@@ -490,6 +490,11 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     for (int j = 0; j < 16; ++j)
                         p[j] = __fadd2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
                                           *reinterpret_cast<const float2 *>(bias + 2 * j));
+                    // Rows past the last are zeros times W, NaN where it holds an infinity: kept out of the column sums.
+                    if (MODE == LIN_GRAD && row0 + lane >= args.M) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) p[j] = make_float2(0.f, 0.f);
+                    }
                     uint8_t *row = ob + lane * 64;
                     const int swz = (lane >> 1) & 3;
                     if (MODE == LIN_GRAD && args.act == LIN_RELU)

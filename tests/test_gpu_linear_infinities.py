@@ -96,3 +96,10 @@ def test_infinity_in_a_row_of_w(rows, k, n):
     w[n // 2, 3], w[n - 1, 5] = np.inf, -np.inf
     assert (x[:, [3, 5]] != 0).all()
     check(x, w, b, dy, "sigmoid")
+
+
+@pytest.mark.parametrize("rows", [100, 128, 20000 + 64])
+@pytest.mark.parametrize("k,n", SIZES[5:])
+def test_infinity_in_a_row_of_w_several_products(rows, k, n):
+    """The same where D is a product of its own."""
+    test_infinity_in_a_row_of_w(rows, k, n)
