@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
         if (!ok) break;
         if (pos == 0) key = key_bits(s + 4);  // the warp's next group
         float2 *rowv = reinterpret_cast<float2 *>(smem + OFF_ROW) + warp * 32;
+        uint32_t empty;  // queries without weight, the same in every warp: past the last, or with no logit over -inf
         {
             float4 v[4];
 #pragma unroll
@@ -408,6 +409,13 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
             }
             const float inv = total == 0.f ? 0.f : 1.f / total;  // a query without a valid key: P = 0
             rowv[lane] = make_float2(own * inv, -dots * inv);
+            empty = __ballot_sync(0xffffffffu, total == 0.f);
+            // Their q and dO may hold anything, and 0 times it would not hide it in dk and dv. (Every warp is done with
+            // its scores: the products below are the tiles' last readers.)
+            if ((empty >> lane) & 1u) {
+                *reinterpret_cast<uint4 *>(smem + OFF_Q + st * TILE + lane * 64 + 16 * warp) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(smem + OFF_DO + st * TILE + lane * 64 + 16 * warp) = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         __syncwarp();
         // P and dS, each rounded once to bf16, the type of the products' other operands.
@@ -424,6 +432,17 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
                     const float2 d = __fmul2_rn(p, __fadd2_rn(dp[mt][nt][r], nd));
                     pb[nt][r] = pack_bf16x2(p.x, p.y);
                     ds[nt][r] = pack_bf16x2(d.x, d.y);
+                }
+            }
+            if (empty != 0u || vmask != 0xFFFFFFFFu) {
+                // dS is 0 there, also where the query's sums are not numbers (P is written as 0, or to a masked
+                // key's row of dv, which is not kept).
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const uint32_t two = vmask >> (8 * nt + 2 * quad);
+                    const uint32_t kept = ((two & 1u) ? 0xFFFFu : 0u) | ((two & 2u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) ds[nt][r] &= (empty >> (16 * mt + 8 * r + grp)) & 1u ? 0u : kept;
                 }
             }
             stsm4(pt + 1024 * mt, pb[0][0], pb[0][1], pb[1][0], pb[1][1]);
@@ -482,7 +501,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) o[x][r] = pack_bf16x2(dq[x][r].x * scale, dq[x][r].y * scale);
+                for (int r = 0; r < 2; ++r)
+                    o[x][r] = (empty >> (q0 + 8 * r + grp)) & 1u ? 0u : pack_bf16x2(dq[x][r].x * scale, dq[x][r].y * scale);
             uint8_t *out = smem + OFF_V + base * TILE + warp * 512;
             stsm4(smem_u32(out) + s32, o[0][0], o[0][1], o[1][0], o[1][1]);
             fence_proxy_async_smem();
