@@ -23,9 +23,9 @@
  * activation and residual in fp32, one rounding to bf16 at the end. The backward
  * rounds D to bf16 before it enters the products dx and dW (with identity or relu
  * D is dy or 0, exactly); db sums D before that rounding. Where p is so near 0
- * that fp32 cannot tell its sign (judged by the size of its row's sums), relu'
- * takes p again in 64 bits. Gradients have the
- * parameters' type. Every sum is taken in a fixed order, so equal calls give equal
+ * that its sums' rounding could turn its sign (under a bound from the norms of its
+ * rows of x and W), relu' takes p again in 64 bits: the sign is right down to
+ * 2^-53 of the products' sizes. Gradients have the parameters' type. Every sum is taken in a fixed order, so equal calls give equal
  * bits.
  *
  * Ownership, threading and errors follow trimul.h: the caller owns every buffer,

@@ -51,7 +51,8 @@ constexpr int BAR_BYTES = 384;
 // x in bf16, and the rest of x's share as 16 KB tiles of codes. Two tiles of dy, and 32 KB of dx blocks.
 __host__ __device__ constexpr int xbufs(int chunks) { return 4 - chunks; }
 __host__ __device__ constexpr int cbufs(int chunks) { return 2 * (3 - chunks); }
-constexpr size_t SMEM = 1024 + 7 * (size_t)TILE + 1024 + BAR_BYTES;
+constexpr int XNORM = 2 * 128 * 2;        // relu: norms of two tiles' rows of x, bf16
+constexpr size_t SMEM = 1024 + 7 * (size_t)TILE + 1024 + BAR_BYTES + XNORM;
 static_assert(SMEM <= 232448, "shared memory budget");
 constexpr int TMEM_COLS = 512, DX_COL = 384;
 }  // namespace lb
@@ -146,8 +147,10 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     uint8_t *codes = xbuf + TILE;                       // kHeld8: [XB]
     uint8_t *dbuf = xbuf + xbufs(CHUNKS) * TILE;        // [2] dy, then D
     uint8_t *obuf = dbuf + 2 * TILE;                    // [WORKERS] 2 KB; kPair: [8] 4 KB
-    float *fbuf = reinterpret_cast<float *>(obuf + WORKERS * OUT);  // bias [256]; at the end db sums
+    float *fbuf = reinterpret_cast<float *>(obuf + WORKERS * OUT);  // bias [256]
+    uint32_t *rbuf = reinterpret_cast<uint32_t *>(fbuf);  // relu: the bias's bf16 below the norm of W's row, bf16 too
     uint64_t *bars = reinterpret_cast<uint64_t *>(fbuf + 256);
+    __nv_bfloat16 *xnorm = reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(bars) + BAR_BYTES);  // [2][128]
     uint64_t *wfull = bars;            // W landed
     uint64_t *xfull = bars + 1;        // [XB] x (kHeld8: codes) landed
     uint64_t *xfree = bars + 5;        // [XB] products reading x are done (kHeld8: codes read, WORKERS arrivals)
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
     uint64_t *sfree = bars + 32;       // kPair: [8] the peer has room for the next part
     volatile uint32_t *sent = reinterpret_cast<volatile uint32_t *>(bars + 40);  // kPair: [8] parts the peer has sent
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 44);
+    uint64_t *nready = bars + 45;      // relu: the norms of a tile's rows are written (WORKERS arrivals)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,6 +193,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         mbar_init(dxfull, 1);
         mbar_init(dxfree, WORKERS);
         mbar_init(drain, 1);
+        mbar_init(nready, WORKERS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
             mbar_init(&dready[i], WORKERS);
@@ -213,8 +218,10 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < 128 * CHUNKS; i += THREADS)
-        fbuf[i] = (args.bias && i < n_mine) ? __bfloat162float(args.bias[n_first + i]) : 0.f;
+    for (int i = threadIdx.x; i < 128 * CHUNKS; i += THREADS) {
+        const uint32_t b = (args.bias && i < n_mine) ? reinterpret_cast<const uint16_t *>(args.bias)[n_first + i] : 0u;
+        rbuf[i] = ACT == LIN_RELU ? b : b << 16;
+    }
     tc_fence_before();
     __syncthreads();
     if (kPair) cluster_sync();  // the peer's barriers are initialised
@@ -353,7 +360,41 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             return (kHeld8 && t < my_tiles && r < args.rows && cblk < kblk) ? (uint32_t)__ldg(args.scales + r * kblk + cblk) : 0u;
         };
         uint32_t scale_next = kHeld8 ? scale_of(0) : 0u;
+        // relu: the norms that bound p's rounding, rounded up to bf16: W's once, x's for each tile, eight rows a warp. A
+        // tile's go to the buffer of the tile before the last, which every warp has left when all have written the
+        // last one's. kHeld8: with the conversion, whose threads have the values in hand, and whose barrier covers them.
+        auto norms = [&](const uint8_t *tile) {
+            float s[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint2 v = tile_quad(tile, 8 * ew + i, lane);
+                s[i] = add_squares(add_squares(0.f, v.x), v.y);
+            }
+            return sums_of_8(s, lane);
+        };
+        auto write_w_norms = [&]() {
+            if (!warp_wait(wfull, 0, abort_flag, ctl, SITE_LBW | 14, 0)) return false;
+#pragma unroll 1
+            for (int cc = 0; cc < CHUNKS; ++cc) {
+                const __nv_bfloat16 v = __float2bfloat16_ru(norm_of(norms(wbuf + cc * TILE)));
+                if ((lane & 3) == 0) reinterpret_cast<__nv_bfloat16 *>(rbuf + cc * 128 + 8 * ew + (lane >> 2))[1] = v;
+            }
+            return true;
+        };
+        auto write_x_norm = [&](int t, float squares) {  // of row 8 ew + lane / 4
+            if ((lane & 3) == 0) xnorm[(t & 1) * 128 + 8 * ew + (lane >> 2)] = __float2bfloat16_ru(norm_of(squares));
+        };
+        auto write_norms = [&](int t) {
+            if (t == 0 && !write_w_norms()) return false;
+            if (!warp_wait(&xfull[t % XB], (uint32_t)(t / XB) & 1u, abort_flag, ctl, SITE_LBW | 14, t)) return false;
+            write_x_norm(t, norms(xbuf + (t % XB) * TILE));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(nready);
+            return true;
+        };
+
         auto convert = [&](int t) {
+            if (ACT == LIN_RELU && t == 0 && !write_w_norms()) return false;
             if (!warp_wait(&xfull[t % XB], (uint32_t)(t / XB) & 1u, abort_flag, ctl, SITE_LBW | 8, t)) return false;
             if (t > 0 && !warp_wait(xdone, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 9, t)) return false;
             const uint32_t s = scale_next;
@@ -361,6 +402,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             const float size = __uint_as_float(s ? s << 23 : 0x00400000u);  // 2^(s - 127)
             const uint8_t *src = codes + (t % XB) * CODES + crow * 128;
             uint8_t *dst = xbuf + (cblk >> 1) * HALF + crow * 128;
+            float squares = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + (((2 * cblk + i) ^ (crow & 7)) << 4));
@@ -371,10 +413,15 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                     const __half2_raw hv = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hv));
                     o[j] = pack_bf16x2(f.x * size, f.y * size);
+                    if (ACT == LIN_RELU) squares = add_squares(squares, o[j]);
                 }
                 const int ch = 4 * (cblk & 1) + 2 * i;
                 *reinterpret_cast<uint4 *>(dst + ((ch ^ (crow & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (crow & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            if (ACT == LIN_RELU) {
+                squares += __shfl_xor_sync(0xffffffffu, squares, 1);
+                write_x_norm(t, squares + __shfl_xor_sync(0xffffffffu, squares, 2));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -390,7 +437,6 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             const int t = u / CHUNKS, c = u - t * CHUNKS, a = u % PRE, db = u & 1;
             give_room();
             float2 p[16];  // [16-row half][8-column block][row, row + 8]
-            float top = 0.f;  // relu: the largest sum, before its bias
             if (has_p) {
                 if (!warp_wait(&pfull[a], (uint32_t)(u / PRE) & 1u, abort_flag, ctl, SITE_LBW | 10, u)) return false;
                 tc_fence_after();
@@ -405,14 +451,14 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 if (lane == 0) mbar_arrive(&pfree[a]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 bv = *reinterpret_cast<const float2 *>(fbuf + c * 128 + 32 * h + 8 * j + 2 * (lane & 3));
+                    const int col = c * 128 + 32 * h + 8 * j + 2 * (lane & 3);
+                    const float2 bv = ACT == LIN_RELU ? make_float2(__uint_as_float(rbuf[col] << 16), __uint_as_float(rbuf[col + 1] << 16))
+                                                      : *reinterpret_cast<const float2 *>(fbuf + col);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         float2 &y = p[(x >> 1) * 8 + 2 * j + (x & 1)];
                         const uint32_t *r = &v[x >> 1][4 * j + 2 * (x & 1)];
-                        const float2 sum = make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
-                        if (ACT == LIN_RELU) top = fmaxf(top, fmaxf(fabsf(sum.x), fabsf(sum.y)));
-                        y = __fadd2_rn(sum, bv);
+                        y = __fadd2_rn(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])), bv);
                     }
                 }
             }
@@ -421,28 +467,24 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             float2 dsum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             uint32_t keep = 0xFFFFFFFFu;  // relu: bit 2 i + e of value p[i].x or .y
             if (ACT == LIN_RELU) {
-                // The sign of a p next to 0 is taken again in 64 bits (see linear_tc.cu).
+                // Where p is under the bound of its rounding (linear_act.cuh) its sign is taken again in 64 bits.
                 uint32_t check = 0;
                 keep = 0;
-                const float near_ = top * (16.f * 2.384185791015625e-7f);
+                if (c == 0 && !warp_wait(kHeld8 ? xready : nready, (uint32_t)t & 1u, abort_flag, ctl, SITE_LBW | 14, u)) return false;
+                float bound[4];  // of rows 16 (x >> 1) + 8 (x & 1) + lane / 4
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    keep |= ((p[i].x > 0.f ? 1u : 0u) | (p[i].y > 0.f ? 2u : 0u)) << (2 * i);
-                    check |= ((fabsf(p[i].x) < near_ ? 1u : 0u) | (fabsf(p[i].y) < near_ ? 2u : 0u)) << (2 * i);
-                }
-                // Rows and columns outside the matrices (p = 0 there) have nothing to decide.
+                for (int x = 0; x < 4; ++x)
+                    bound[x] = sign_bound(args.k) * __bfloat162float(xnorm[(t & 1) * 128 + 32 * q + 8 * x + (lane >> 2)]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (c * 128 + 32 * h + 8 * x >= n_mine) check &= ~(0x000F000Fu << (4 * x));  // column block x
-                    const uint32_t row_bits = 0x3333u << (2 * (x & 1)) << (16 * (x >> 1));       // rows 8 x + lane / 4
-                    if ((long long)row0(t) + 32 * q + 8 * x + (lane >> 2) >= args.rows) check &= ~row_bits;
-                }
-                if (__any_sync(0xffffffffu, check != 0)) {
-                    // x and W are read here as they landed: observe their barriers.
-                    uint64_t *xb = kHeld8 ? xready : &xfull[t % XB];
-                    if (!warp_wait(wfull, 0, abort_flag, ctl, SITE_LBW | 14, u) ||
-                        !warp_wait(xb, (uint32_t)(kHeld8 ? t : t / XB) & 1u, abort_flag, ctl, SITE_LBW | 14, u))
-                        return false;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t *w = rbuf + c * 128 + 32 * h + 8 * j + 2 * (lane & 3);
+                    const float w0 = __uint_as_float(w[0] & 0xFFFF0000u), w1 = __uint_as_float(w[1] & 0xFFFF0000u);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int i = (x >> 1) * 8 + 2 * j + (x & 1);
+                        keep |= ((p[i].x > 0.f ? 1u : 0u) | (p[i].y > 0.f ? 2u : 0u)) << (2 * i);
+                        check |= ((fabsf(p[i].x) < bound[x] * w0 ? 1u : 0u) | (fabsf(p[i].y) < bound[x] * w1 ? 2u : 0u)) << (2 * i);
+                    }
                 }
                 for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
                     const int src = __ffs(who) - 1;
@@ -455,7 +497,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                         double sum = (double)xa.x * wa.x + (double)xa.y * wa.y + (double)xb.x * wb.x + (double)xb.y * wb.y;
 #pragma unroll
                         for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                        if (lane == src) keep = (keep & ~(1u << bit)) | (sum + (double)fbuf[c * 128 + col] > 0.0 ? 1u << bit : 0u);
+                        if (lane == src) keep = (keep & ~(1u << bit)) | (sum + (double)__uint_as_float(rbuf[c * 128 + col] << 16) > 0.0 ? 1u << bit : 0u);
                     }
                 }
             }
@@ -538,6 +580,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
         };
 
         const bool has_dx = args.has_dx != 0;
+        if (ACT == LIN_RELU && !kHeld8 && my_tiles > 0) ok = write_norms(0);
         for (int t = 0; ok && t < my_tiles; ++t) {
             if (kHeld8) {
                 // x first: p of the tile is then computed while dx of the tile before is drained.
@@ -548,6 +591,8 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
                 if (!(ok = make_d(t * CHUNKS + c))) break;
                 if (!kHeld8 && c == 0 && has_dx && t > 0 && !(ok = drain_dx(t - 1))) break;
             }
+            // The next tile's norms, so that its D need not wait for them.
+            if (ACT == LIN_RELU && !kHeld8 && ok && t + 1 < my_tiles) ok = write_norms(t + 1);
         }
         if (ok && has_dx && my_tiles > 0) ok = drain_dx(my_tiles - 1);
         if (lane == 0) tma_store_wait_all<0>();

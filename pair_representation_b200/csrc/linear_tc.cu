@@ -41,7 +41,7 @@ constexpr int THREADS = (2 + EPI_WARPS) * 32;
 constexpr int WBUF = 4096;                  // a drain warp's: two blocks of 32 rows x 32 bf16, or one of fp32
 constexpr int OUT_BYTES = EPI_WARPS * WBUF;
 constexpr int BIAS_BYTES = EPI_WARPS * 64 * 4;  // each drain warp's own copy of its columns' bias
-constexpr int ONES_BYTES = 16 * BK * 2;     // 16 rows of ones (LIN_WG)
+constexpr int ONES_BYTES = 16 * BK * 2;     // 16 rows of ones (LIN_WG), or (LIN_GRAD) the norms of 256 rows of W and 2 x 128 of x
 constexpr int BAR_BYTES = 512;
 constexpr int RES_BYTES = 65536;            // resident slab of B
 constexpr int TMEM_COLS = 512;
@@ -136,26 +136,40 @@ __device__ __forceinline__ void finish(int act, float2 (&p)[16], uint8_t *row, i
     else finish_row<MODE, LIN_SILU, kE>(p, row, swz);
 }
 
-// relu's gradient of one accumulator row: keep E where p > 0. The accumulator's rounding decides
-// the sign of a p next to 0, and a wrong one is not a small error of the gradient but the
-// whole of dy: where |p| is under the bound of that rounding (one step of 2^-22 of the row's
-// largest sum for each 16 products), the warp takes the row's product again in 64 bits,
-// one place at a time. At random inputs about 1 in 10^5 places.
-__device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[16], const float *bias, uint8_t *row, int swz,
-                                                     const LinearArgs &a, int r, int col0, int lane) {
-    float top = 0.f;
-    uint32_t keep = 0, check = 0;
+// Norms of eight rows of a matrix [rows][K] from row `first`, 0 past the last: lane l returns that of row
+// first + (l >> 2).
+__device__ __forceinline__ float norms_of_8(const __nv_bfloat16 *m, int first, int rows, int K, int lane) {
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 8 * lane; k < K; k += 256) {  // K is a multiple of 8
+        uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(fabsf(v[j].x - bias[2 * j]), fabsf(v[j].y - bias[2 * j + 1])));
-    const float near_ = top * (float)(4 * a.kblocks + 8) * 2.384185791015625e-7f;
+        for (int i = 0; i < 8; ++i)
+            v[i] = first + i < rows ? *reinterpret_cast<const uint4 *>(m + (size_t)(first + i) * K + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = add_squares(add_squares(add_squares(add_squares(s[i], v[i].x), v[i].y), v[i].z), v[i].w);
+    }
+    return norm_of(sums_of_8(s, lane));
+}
+
+// The products of two bf16 pairs, exact in fp32, in 64 bits.
+__device__ __forceinline__ double pair_product(uint32_t x, uint32_t w) {
+    return (double)(__uint_as_float(x << 16) * __uint_as_float(w << 16)) +
+           (double)(__uint_as_float(x & 0xFFFF0000u) * __uint_as_float(w & 0xFFFF0000u));
+}
+
+// relu's gradient of one accumulator row: keep E where p > 0. Where p is under the bound of its rounding
+// (linear_act.cuh; `bound` has the row's norm of x in it, wnorm those of W), the warp takes the row's product
+// again, one place at a time.
+__device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[16], const float *bias, uint8_t *row, int swz,
+                                                     const LinearArgs &a, int r, int col0, int lane, float bound,
+                                                     const float *wnorm) {
+    uint32_t keep = 0, check = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
         const float p = j & 1 ? v[j >> 1].y : v[j >> 1].x;
         keep |= (uint32_t)(p > 0.f) << j;
-        check |= (uint32_t)(fabsf(p) < near_) << j;
+        check |= (uint32_t)(fabsf(p) < bound * wnorm[j]) << j;
     }
-    if (r >= a.M) check = 0;
-    if (a.N - col0 < 32) check &= (1u << (a.N - col0)) - 1;
     for (unsigned who = __ballot_sync(0xffffffffu, check != 0); who; who &= who - 1) {
         const int src = __ffs(who) - 1;
         const __nv_bfloat16 *xr = a.x + (size_t)(r - lane + src) * a.K;
@@ -163,8 +177,10 @@ __device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[16], const floa
             const int j = __ffs(left) - 1;
             const __nv_bfloat16 *wr = a.w + (size_t)(col0 + j) * a.K;
             double sum = 0.0;
-            for (int k = lane; k < a.K; k += 32)
-                sum += (double)__bfloat162float(xr[k]) * (double)__bfloat162float(wr[k]);
+            for (int k = 8 * lane; k < a.K; k += 256) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(xr + k), w = *reinterpret_cast<const uint4 *>(wr + k);
+                sum += (pair_product(x.x, w.x) + pair_product(x.y, w.y)) + (pair_product(x.z, w.z) + pair_product(x.w, w.w));
+            }
 #pragma unroll
             for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
             if (lane == src) keep = (keep & ~(1u << j)) | (uint32_t)(sum + (double)bias[j] > 0.0) << j;
@@ -240,7 +256,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     uint64_t *tempty = tfull + 2;           // [2] accumulator drained (EPI_WARPS arrivals)
     uint64_t *efull = tempty + 2;           // [EPI_WARPS][2] E block landed
     uint64_t *drain = efull + 2 * EPI_WARPS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *nready = drain + 1;           // relu's LIN_GRAD: norms of a tile's rows written (EPI_WARPS arrivals)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(nready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -259,6 +276,7 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         }
         for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(&efull[i], 1);
         mbar_init(drain, 1);
+        mbar_init(nready, EPI_WARPS);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmA);
@@ -441,12 +459,31 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < COLS; ++i) colsum[i] = 0.f;
+        // relu's gradient: the norms that bound p's rounding, of W's rows of this column tile and of each tile's rows of
+        // x, eight rows a warp, read again through L2 while the products run. A tile's go to the buffer of the tile before
+        // the last, which every warp has left when all have written the last one's.
+        const bool relu_grad = MODE == LIN_GRAD && args.act == LIN_RELU;
+        float *wnorm = reinterpret_cast<float *>(ones), *xnorm = wnorm + 256;
+        if (relu_grad) {
+            const int n0 = ((int)blockIdx.x % args.col_tiles) * BN;
+            for (int j = 8 * ew; j < BN; j += 8 * EPI_WARPS) {
+                const float norm = norms_of_8(args.w, n0 + j, args.N, args.K, lane);
+                if ((lane & 3) == 0) wnorm[j + (lane >> 2)] = norm;
+            }
+        }
         bool ok = true;
         Tiles<MODE> t(args);
         while (ok && t.next()) {
             const int acc = lt & 1;
+            if (relu_grad) {
+                const float norm = norms_of_8(args.x, t.rt * BM + 8 * ew, args.M, args.K, lane);
+                if ((lane & 3) == 0) xnorm[acc * BM + 8 * ew + (lane >> 2)] = norm;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(nready);
+            }
             if (!warp_wait(&tfull[acc], (uint32_t)(lt >> 1) & 1u, abort_flag, ctl, SITE_LIN | 6, t.rt)) break;
             tc_fence_after();
+            if (relu_grad && !warp_wait(nready, (uint32_t)lt & 1u, abort_flag, ctl, SITE_LIN | 8, t.rt)) break;
             const int top = t.rt * (HIGH * BM) + 32 * q;
 #pragma unroll
             for (int ci = 0; ci < MINE; ++ci) {
@@ -498,7 +535,8 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
                     uint8_t *row = ob + lane * 64;
                     const int swz = (lane >> 1) & 3;
                     if (MODE == LIN_GRAD && args.act == LIN_RELU)
-                        finish_row_relu_grad(p, bias, row, swz, args, row0 + lane, col, lane);
+                        finish_row_relu_grad(p, bias, row, swz, args, row0 + lane, col, lane,
+                                             sign_bound(args.K) * xnorm[acc * BM + 32 * q + lane], wnorm + ch * CHUNK);
                     else if (MODE == LIN_GRAD || has_e)
                         finish<MODE, true>(args.act, p, row, swz);
                     else
