@@ -404,31 +404,6 @@ def atomattn_device_status(params: AtomAttnParams, stream=None):
     return rc, list(d)
 
 
-def atom_attention(q, k, v, bias=None, atom_mask=None, out=None, workspace=None, stream=None):
-    """Windowed atom attention (include/atomattn.h) on bf16 device tensors.
-
-    q, k, v: [batch][n_atoms][heads][32]; bias: [batch][ceil(n_atoms/32)][heads][32][128]
-    or None; atom_mask: [batch][n_atoms] or None. Returns out (allocated if None)."""
-    import torch
-    if q.dim() != 4 or q.shape[-1] != 32 or k.shape != q.shape or v.shape != q.shape:
-        raise ValueError("q, k, v must be [batch, n_atoms, heads, 32] of one shape")
-    for t in (q, k, v, bias, atom_mask):
-        if t is not None and (t.dtype != torch.bfloat16 or not t.is_contiguous()):
-            raise ValueError("inputs must be contiguous bf16")
-    B, n, H, _ = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = torch.zeros(atomattn_workspace_size(), dtype=torch.uint8, device=q.device)
-    p = AtomAttnParams()
-    p.batch, p.n_atoms, p.heads, p.head_dim = B, n, H, 32
-    p.q, p.k, p.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    p.bias, p.atom_mask = _ptr(bias), _ptr(atom_mask)
-    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    atomattn_forward(p, out, stream)
-    return out, p
-
-
 def atomattn_backward(params: AtomAttnParams, dout, grads: AtomAttnGrads, stream=None, check=True) -> int:
     rc = lib().atomattn_backward(ctypes.byref(params), _ptr(dout), ctypes.byref(grads), _stream(stream))
     if check:
@@ -500,6 +475,47 @@ def _status_workspace(index: int):
     return ws
 
 
+def _attention_shape(what, q, bias, atom_mask, like):
+    """q's batch, atoms and heads; the kernels take every other tensor's size from these."""
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != 32 or any(t is not None and t.shape != shape for t in like):
+        raise ValueError(f"{what}: q, k, v, dout and out must be [batch, n_atoms, heads, 32] of one shape")
+    B, n, H, _ = shape
+    if bias is not None and bias.shape != (B, (n + 31) // 32, H, 32, 128):
+        raise ValueError(f"{what}: bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
+    if atom_mask is not None and atom_mask.shape != (B, n):
+        raise ValueError(f"{what}: atom_mask must be [batch, n_atoms]")
+    return B, n, H
+
+
+def atom_attention(q, k, v, bias=None, atom_mask=None, out=None, workspace=None, stream=None):
+    """Windowed atom attention (include/atomattn.h) on bf16 device tensors.
+
+    q, k, v: [batch][n_atoms][heads][32]; bias: [batch][ceil(n_atoms/32)][heads][32][128]
+    or None; atom_mask: [batch][n_atoms] or None. Returns out (allocated if None) and the call's
+    AtomAttnParams, whose status atomattn_device_status reads."""
+    torch = _T or _load()
+    B, n, H = _attention_shape("atom_attention", q, bias, atom_mask, (k, v, out))
+    if out is not None and out.dtype is not _BF16:
+        raise ValueError("atom_attention: tensors must be contiguous bf16")
+    index = q.get_device()
+    _need_bf16("atom_attention", index, (q, k, v, bias, atom_mask, out))
+    if workspace is not None:
+        _need_workspace("atom_attention", index, workspace)
+    if _current_device() != index or stream is not None and _stream(stream) != _raw_stream(index):
+        return _run_on(index, stream, (q, k, v, bias, atom_mask, out, workspace),
+                       lambda: atom_attention(q, k, v, bias, atom_mask, out, workspace))
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = torch.zeros(atomattn_workspace_size(), dtype=torch.uint8, device=q.device)
+    p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask),
+                       workspace.data_ptr(), workspace.numel(), 0)
+    p.kept = workspace  # its memory stays while the status may be asked for
+    atomattn_forward(p, out, _raw_stream(index))
+    return out, p
+
+
 def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=None, stream=None):
     """Gradients of sum(atom_attention(q, k, v, bias, atom_mask) * dout) (include/atomattn.h).
 
@@ -507,14 +523,7 @@ def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=
     without bias. `workspace` (atomattn_workspace_size() bytes): where device_status finds this
     call's status; without one, calls of a device share a status word."""
     torch = _T or _load()
-    shape = q.shape
-    if len(shape) != 4 or shape[3] != 32 or k.shape != shape or v.shape != shape or dout.shape != shape:
-        raise ValueError("q, k, v, dout must be [batch, n_atoms, heads, 32] of one shape")
-    B, n, H, _ = shape
-    if bias is not None and bias.shape != (B, (n + 31) // 32, H, 32, 128):
-        raise ValueError("bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
-    if atom_mask is not None and atom_mask.shape != (B, n):
-        raise ValueError("atom_mask must be [batch, n_atoms]")
+    B, n, H = _attention_shape("atom_attention_backward", q, bias, atom_mask, (k, v, dout))
     index = q.get_device()
     _need_bf16("atom_attention_backward", index, (q, k, v, dout, bias, atom_mask))
     if workspace is not None:
@@ -966,11 +975,9 @@ class AtomAttention:
         return linear(x, self.tensors[f"linear_{name}.weight"], self.tensors.get(f"linear_{name}.bias"), residual)
 
     def _core(self, x, bias, atom_mask):
-        import torch
         shape = tuple(x.shape[:2]) + (self.heads, 32)
         q, k, v = (self._linear(n, x).view(shape) for n in "qkv")
-        with torch.cuda.device(q.device):  # atom_attention runs on the current device
-            return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
+        return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
 
     def _check(self, x):
         if len(x.shape) != 3 or x.shape[2] != self.c_atom:

@@ -1,0 +1,57 @@
+"""What the layers' calls refuse before any work is enqueued, and the sizes they ask for (no GPU needed)."""
+import pytest
+import torch
+
+import pair_representation_b200 as tm
+from pair_representation_b200 import build as tmbuild
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    tmbuild.build()
+
+
+def _attention_arguments():
+    """Right shapes, one wrong at a time: a kernel takes each tensor's size from q's."""
+    q = torch.zeros(2, 70, 3, 32, dtype=BF16)
+    bias, mask = torch.zeros(2, 3, 3, 32, 128, dtype=BF16), torch.ones(2, 70, dtype=BF16)
+    yield q, bias[:1], mask, None
+    yield q, bias[:, :2], mask, None
+    yield q, bias[:, :, :2], mask, None
+    yield q, bias[..., :96], mask, None
+    yield q, bias.reshape(-1), mask, None
+    yield q, bias, mask[:, :32], None
+    yield q, bias, mask[:1], None
+    yield q, bias, mask.reshape(-1), None
+    yield q, None, mask[:, :69], None
+    yield q, bias, mask, torch.zeros(2, 70, 3, 16, dtype=BF16)
+    yield q, bias, mask, torch.zeros(1, 70, 3, 32, dtype=BF16)
+    yield q, bias, mask, torch.zeros(2, 70, 3, 32)
+
+
+@pytest.mark.parametrize("case", range(12))
+def test_attention_refuses_other_shapes(case):
+    q, bias, mask, out = list(_attention_arguments())[case]
+    with pytest.raises(ValueError) as e:
+        tm.atom_attention(q, q, q, bias, mask, out=out)
+    assert "CUDA device" not in str(e.value)  # found before the tensors' place
+
+
+def test_attention_refuses_tensors_of_the_host():
+    q = torch.zeros(1, 40, 2, 32, dtype=BF16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        tm.atom_attention(q, q, q)
+
+
+@pytest.mark.parametrize("case", range(5))
+def test_the_layer_refuses_a_bias_or_mask_of_another_shape(case, monkeypatch):
+    """The layer's calls give the core their bias and mask as they came: with the projections taken out, on the CPU."""
+    _, bias, mask, _ = list(_attention_arguments())[(0, 1, 3, 5, 6)[case]]
+    layer = tm.AtomAttention(64, 3)
+    monkeypatch.setattr(layer, "_linear", lambda name, x, residual=None: torch.zeros(2, 70, 96, dtype=BF16))
+    x = torch.zeros(2, 70, 64, dtype=BF16)
+    for call in (lambda: layer(x, bias, mask), lambda: layer.backward(x, x, bias, mask)):
+        with pytest.raises(ValueError, match="must be"):
+            call()
