@@ -15,8 +15,7 @@
  *   a slot is valid when its atom lies in [0, n_atoms) and its atom_mask is not
  *   0; a query with no valid slot gets 0.
  *
- * The projections, gating and output projection around this core are per-atom
- * Linear layers and not part of the library.
+ * The projections around this core are per-atom Linear layers (linear.h).
  *
  * Layouts (row-major, contiguous, bf16):
  *   q, k, v, out  [batch][n_atoms][heads][32]
@@ -28,8 +27,8 @@
  * Ownership, threading and errors follow trimul.h: the caller owns every
  * buffer, the call enqueues on `stream` and returns TRIMUL_OK or a negative
  * trimul_status; argument errors are found on the host; a bounded in-kernel
- * wait that runs out is recorded in the workspace's status word
- * (atomattn_device_status). Computed on tcgen05 tensor cores (bf16 operands,
+ * wait that runs out is recorded in the status word, the workspace's or the
+ * caller's own (atomattn_device_status). Computed on tcgen05 tensor cores (bf16 operands,
  * fp32 logits, softmax and accumulation; the probabilities enter the second
  * product as bf16).
  */
@@ -53,9 +52,11 @@ typedef struct atomattn_params {
     void *workspace;        /* device memory, 256-byte aligned, >= atomattn_workspace_size() */
     size_t workspace_bytes;
     uint32_t timeout_ms;    /* bound on each in-kernel wait; 0 = 2000 ms */
+    void *status;           /* NULL: the status word is the workspace's, cleared by each call;
+                               else one that calls do not clear (trimul_status_word) */
 } atomattn_params;
 
-/* Bytes of workspace (the device status word). */
+/* Bytes of workspace (the device status word). With p->status none is needed. */
 size_t atomattn_workspace_size(void);
 
 int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream);
@@ -81,7 +82,8 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
  * input, each other or the workspace. dbias without bias is an error. The atoms'
  * gradients are written for every atom; nothing else is. All pointers must be
  * memory of the current device. p->workspace holds the status word
- * (atomattn_device_status); calls that may overlap in time need their own. */
+ * (atomattn_device_status); calls that may overlap in time need their own, or
+ * p->status. */
 typedef struct atomattn_grads {
     void *dq, *dk, *dv;
     void *dbias;            /* or NULL */

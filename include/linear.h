@@ -31,8 +31,8 @@
  * Ownership, threading and errors follow trimul.h: the caller owns every buffer,
  * a call enqueues on `stream` and returns TRIMUL_OK or a negative trimul_status,
  * argument errors are found on the host before any work is enqueued, and a bounded
- * in-kernel wait that runs out is recorded in the workspace's status word
- * (trimul_linear_device_status). Calls that may overlap in time need workspaces of
+ * in-kernel wait that runs out is recorded in the status word, the workspace's or
+ * the caller's own (trimul_linear_device_status). Calls that may overlap in time need workspaces of
  * their own, captured graphs included. All pointers must be memory of the current
  * device.
  */
@@ -61,9 +61,12 @@ typedef struct trimul_linear_params {
     void *workspace;        /* device memory, 256-byte aligned */
     size_t workspace_bytes;
     uint32_t timeout_ms;    /* bound on each in-kernel wait; 0 = 2000 ms */
+    void *status;           /* NULL: the status word is the workspace's, cleared by each call;
+                               else one that calls do not clear (trimul_status_word) */
 } trimul_linear_params;
 
-/* Bytes of workspace of the forward (the device status word). */
+/* Bytes of workspace of the forward (the device status word). With p->status, a
+ * call whose workspace would hold nothing else needs none (workspace NULL). */
 size_t trimul_linear_workspace_size(void);
 
 /* y = act(x W^T + b) + residual (residual may be NULL). Asynchronous. */
@@ -106,7 +109,7 @@ size_t trimul_linear_backward_workspace_size(long long rows, int in_features, in
 int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy, const trimul_linear_params *p,
                            void *dx, void *dw, void *db, trimul_stream_t stream);
 
-/* Synchronises `stream`, then reads the workspace's status word: TRIMUL_OK,
+/* Synchronises `stream`, then reads the params' status word: TRIMUL_OK,
  * TRIMUL_ERR_TIMEOUT or TRIMUL_ERR_DEVICE; detail[4] (optional) receives code,
  * site, block, aux. */
 int trimul_linear_device_status(const trimul_linear_params *p, trimul_stream_t stream, int *detail);

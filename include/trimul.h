@@ -127,6 +127,20 @@ int trimul_workspace_views(const trimul_params *p, void **a, void **b, void **x,
  * trimul_forward_noalloc uses on the current device. */
 int trimul_device_status(const trimul_params *p, trimul_stream_t stream, int *detail);
 
+/* A status word apart from any workspace, for the calls whose params have a
+ * `status` field (linear.h, atomattn.h): they do not clear it, so it holds the
+ * first failure since it was 0, whichever call had it. 16 bytes of device memory,
+ * 16-byte aligned, zeroed by the caller before its first use; any number of
+ * calls may share one, also at the same time and from captured graphs.
+ *
+ * trimul_status_word gives the one that the library itself keeps for the current
+ * device, until the process exits. */
+int trimul_status_word(void **word);
+
+/* Synchronises `stream`, then reads such a word as trimul_device_status reads a
+ * workspace's and, where it held a failure, sets it back to 0. */
+int trimul_status_take(void *word, trimul_stream_t stream, int *detail);
+
 /* Static description of a status code. */
 const char *trimul_error_string(int code);
 

@@ -38,6 +38,7 @@ ERR = {v: k for k, v in STATUS.items()}
 # Every symbol include/trimul.h, include/atomattn.h and include/linear.h declare.
 EXPORTS = ("trimul_workspace_size", "trimul_workspace_size_dtype", "trimul_forward", "trimul_prologue",
            "trimul_contract", "trimul_epilogue", "trimul_workspace_views", "trimul_device_status",
+           "trimul_status_word", "trimul_status_take",
            "trimul_error_string", "trimul_last_error_detail", "trimul_version", "trimul_forward_noalloc",
            "trimul_backward", "trimul_backward_workspace_size", "trimul_backward_workspace_size_rows",
            "trimul_backward_block_rows",
@@ -99,6 +100,7 @@ class AtomAttnParams(ctypes.Structure):
         ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
         ("bias", ctypes.c_void_p), ("atom_mask", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("timeout_ms", ctypes.c_uint32),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -115,6 +117,7 @@ class LinearParams(ctypes.Structure):
         ("rows", ctypes.c_longlong), ("in_features", ctypes.c_int), ("out_features", ctypes.c_int),
         ("act", ctypes.c_int), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("timeout_ms", ctypes.c_uint32),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -148,6 +151,8 @@ def lib():
         L.trimul_workspace_views.argtypes = [PP, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P),
                                              ctypes.POINTER(S)]
         L.trimul_device_status.argtypes = [PP, P, ctypes.POINTER(ctypes.c_int)]
+        L.trimul_status_word.argtypes = [ctypes.POINTER(P)]
+        L.trimul_status_take.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
         L.trimul_error_string.argtypes = [I]
         L.trimul_error_string.restype = ctypes.c_char_p
         L.trimul_last_error_detail.argtypes = []
@@ -191,7 +196,8 @@ def lib():
                   "trimul_act8_pack", "trimul_act8_unpack"):
             getattr(L, f).restype = I
         for f in ("trimul_forward", "trimul_forward_noalloc", "trimul_prologue", "trimul_contract", "trimul_epilogue",
-                  "trimul_workspace_views", "trimul_device_status", "trimul_version", "trimul_backward",
+                  "trimul_workspace_views", "trimul_device_status", "trimul_status_word", "trimul_status_take",
+                  "trimul_version", "trimul_backward",
                   "atomattn_forward", "atomattn_device_status", "trimul_forward_mxfp8", "trimul_contract_mxfp8",
                   "trimul_mxfp8_views", "trimul_prologue_mxfp8", "trimul_mma_mxfp8", "trimul_prologue_rows", "trimul_contract_channels", "trimul_epilogue_rows"):
             getattr(L, f).restype = I
@@ -384,6 +390,20 @@ def trimul_device_status(params: TrimulParams, stream=None):
     return rc, list(d)
 
 
+def trimul_status_word() -> int:
+    """Device address of the status word that the library keeps for the current device."""
+    word = ctypes.c_void_p()
+    _check(lib().trimul_status_word(ctypes.byref(word)), "trimul_status_word")
+    return word.value
+
+
+def trimul_status_take(word: int, stream=None):
+    """(code, [code, site, block, aux]) of a status word that calls do not clear, set back to 0 (synchronises)."""
+    d = (ctypes.c_int * 4)()
+    rc = lib().trimul_status_take(word, _stream(stream), d)
+    return rc, list(d)
+
+
 # ---- sequence-local atom attention -------------------------------------------
 
 def atomattn_workspace_size() -> int:
@@ -460,26 +480,25 @@ def _run_on(index: int, stream, tensors, call):
             return out
 
 
-_status = {}  # device index -> status workspace of the calls that are given none
+_words = {}  # device index -> the library's status word there, of the calls that are given no workspace
 
 
-def _status_workspace(index: int):
-    """256 bytes for the status word of a call that the caller gave no workspace: one buffer per
-    device, kept. Calls that overlap share it, which only their status notices. A first call
-    inside a capture takes memory of the graph's own instead."""
-    ws = _status.get(index)
-    if ws is None:
-        ws = _T.zeros(256, dtype=_U8, device=_T.device("cuda", index))
-        if not _T.cuda.is_current_stream_capturing():
-            _status[index] = ws
-    return ws
+def _status_word(index: int) -> int:
+    """Looked up with device `index` current. Its memory is the library's: a captured call's replays write it too."""
+    word = _words.get(index)
+    if word is None:
+        word = _words[index] = trimul_status_word()
+    return word
 
 
 def _attention_shape(what, q, bias, atom_mask, like):
     """q's batch, atoms and heads; the kernels take every other tensor's size from these."""
     shape = q.shape
-    if len(shape) != 4 or shape[3] != 32 or any(t is not None and t.shape != shape for t in like):
-        raise ValueError(f"{what}: q, k, v, dout and out must be [batch, n_atoms, heads, 32] of one shape")
+    if len(shape) != 4 or shape[3] != 32:
+        raise ValueError(f"{what}: q must be [batch, n_atoms, heads, 32]")
+    for t in like:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{what}: q, k, v, dout and out must be of one shape")
     B, n, H, _ = shape
     if bias is not None and bias.shape != (B, (n + 31) // 32, H, 32, 128):
         raise ValueError(f"{what}: bias must be [batch, ceil(n_atoms / 32), heads, 32, 128]")
@@ -516,12 +535,27 @@ def atom_attention(q, k, v, bias=None, atom_mask=None, out=None, workspace=None,
     return out, p
 
 
+def _attention_core(q, k, v, bias, atom_mask):
+    """atom_attention's result alone, its failures kept by the device's status word."""
+    torch = _T or _load()
+    B, n, H = _attention_shape("atom_attention", q, bias, atom_mask, (k, v))
+    index = q.get_device()
+    _need_bf16("atom_attention", index, (q, k, v, bias, atom_mask))
+    if _current_device() != index:
+        return _run_on(index, None, (), lambda: _attention_core(q, k, v, bias, atom_mask))
+    out = torch.empty_like(q)
+    p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(bias), _ptr(atom_mask), None, 0, 0,
+                       _status_word(index))
+    atomattn_forward(p, out, _raw_stream(index))
+    return out
+
+
 def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=None, stream=None):
     """Gradients of sum(atom_attention(q, k, v, bias, atom_mask) * dout) (include/atomattn.h).
 
     Arguments as for atom_attention, dout like q. Returns (dq, dk, dv, dbias), dbias None
     without bias. `workspace` (atomattn_workspace_size() bytes): where device_status finds this
-    call's status; without one, calls of a device share a status word."""
+    call's status; without one, the device's status word keeps a failure."""
     torch = _T or _load()
     B, n, H = _attention_shape("atom_attention_backward", q, bias, atom_mask, (k, v, dout))
     index = q.get_device()
@@ -533,9 +567,9 @@ def atom_attention_backward(q, k, v, dout, bias=None, atom_mask=None, workspace=
                        lambda: atom_attention_backward(q, k, v, dout, bias, atom_mask, workspace))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
     dbias = None if bias is None else torch.empty_like(bias)
-    ws = _status_workspace(index) if workspace is None else workspace
+    ws, size, word = (None, 0, _status_word(index)) if workspace is None else (workspace.data_ptr(), workspace.numel(), None)
     p = AtomAttnParams(B, n, H, 32, q.data_ptr(), k.data_ptr(), v.data_ptr(), None if bias is None else bias.data_ptr(),
-                       None if atom_mask is None else atom_mask.data_ptr(), ws.data_ptr(), ws.numel(), 0)
+                       None if atom_mask is None else atom_mask.data_ptr(), ws, size, 0, word)
     g = AtomAttnGrads(dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if bias is None else dbias.data_ptr())
     rc = _L.atomattn_backward(p, dout.data_ptr(), g, _raw_stream(index))
     if rc:
@@ -592,15 +626,15 @@ def trimul_act8_unpack(codes, scales, rows: int, channels: int, x, stream=None, 
 
 def device_status(workspace, stream=None):
     """(code, [code, site, block, aux]) that the last linear, linear_backward or
-    atom_attention_backward call with this workspace left (synchronises); with a device in the
-    workspace's place, the last such call of that device that was given none."""
+    atom_attention_backward call with this workspace left (synchronises). With a device in the
+    workspace's place: the first failure since this was last asked among that device's calls that were
+    given no workspace, AtomAttention's and captured ones included. Only `stream` (by default the
+    current one) is waited for: work on others may still add one."""
     torch = _T or _load()
     if not isinstance(workspace, torch.Tensor):
         device = torch.device(workspace)
         index = torch.cuda.current_device() if device.index is None else device.index
-        if index not in _status:
-            return 0, [0, 0, 0, 0]
-        workspace = _status[index]
+        return _run_on(index, stream, (), lambda: trimul_status_take(_status_word(index)))
     p = LinearParams()
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
     return _run_on(workspace.get_device(), stream, (), lambda: trimul_linear_device_status(p))
@@ -697,7 +731,7 @@ def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=
     "sigmoid" or "silu". Returns out (allocated if None; it may be the residual itself). Not
     recorded by autograd: linear_backward gives the gradients. `workspace`
     (trimul_linear_workspace_size() bytes): where device_status finds this call's status;
-    without one, calls of a device share a status word."""
+    without one, the device's status word keeps a failure."""
     torch = _T or _load()
     shape = _linear_shape("linear", x.shape, weight, bias, act)
     index = x.get_device()
@@ -715,9 +749,8 @@ def linear(x, weight, bias=None, residual=None, act="none", out=None, workspace=
     y = out if out is not None else torch.empty_like(x) if n == k else x.new_empty(shape)
     rows = x.numel() // k
     if rows and n:
-        ws = _status_workspace(index) if workspace is None else workspace
-        p = LinearParams(rows, k, n, ACTS[act], weight.data_ptr(), None if bias is None else bias.data_ptr(),
-                         ws.data_ptr(), ws.numel(), 0)
+        ws, size, word = (None, 0, _status_word(index)) if workspace is None else (workspace.data_ptr(), workspace.numel(), None)
+        p = LinearParams(rows, k, n, ACTS[act], weight.data_ptr(), None if bias is None else bias.data_ptr(), ws, size, 0, word)
         rc = _L.trimul_linear_forward(x.data_ptr(), None if residual is None else residual.data_ptr(), p, y.data_ptr(),
                                       _raw_stream(index))
         if rc:
@@ -758,12 +791,14 @@ def linear_backward(x, weight, dout, bias=None, act="none", need_dx=True, need_d
             if t is not None:
                 t.zero_()
         return dx, dw, db
-    code, ws = ACTS[act], workspace
+    code, ws, word = ACTS[act], workspace, None
     if ws is None:
+        word = _status_word(index)
         need = _L.trimul_linear_backward_workspace_size(rows, k, n, code, held)
-        ws = _status_workspace(index) if need <= 256 else weight.new_empty(need, dtype=_U8)
-    p = LinearParams(rows, k, n, code, weight.data_ptr(), None if bias is None else bias.data_ptr(), ws.data_ptr(),
-                     ws.numel(), 0)
+        if need > 256:  # more than a status word
+            ws = weight.new_empty(need, dtype=_U8)
+    p = LinearParams(rows, k, n, code, weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                     None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), 0, word)
     rc = _L.trimul_linear_backward(None if held else x.data_ptr(),
                                    Act8Ptrs(x.codes.data_ptr(), x.scales.data_ptr()) if held else None, dout.data_ptr(), p,
                                    dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
@@ -977,7 +1012,7 @@ class AtomAttention:
     def _core(self, x, bias, atom_mask):
         shape = tuple(x.shape[:2]) + (self.heads, 32)
         q, k, v = (self._linear(n, x).view(shape) for n in "qkv")
-        return q, k, v, atom_attention(q, k, v, bias, atom_mask)[0]
+        return q, k, v, _attention_core(q, k, v, bias, atom_mask)
 
     def _check(self, x):
         if len(x.shape) != 3 or x.shape[2] != self.c_atom:

@@ -1,8 +1,8 @@
 // api.cu - the C ABI declared in include/trimul.h: argument checks, workspace
 // carve-up, TMA descriptors and the launch sequence of the three stages.
 //
-// Nothing here allocates device memory or synchronises, except
-// trimul_device_status, whose contract is to synchronise.
+// Nothing here allocates device memory or synchronises, except the calls that
+// read a status word, whose contract is to synchronise.
 #include <cudaTypedefs.h>
 
 #include <cstdio>
@@ -29,6 +29,10 @@ thread_local char g_detail[512];
 void set_detail(const char *what, cudaError_t e) {
     snprintf(g_detail, sizeof g_detail, "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
 }
+
+// The status word of calls whose params name none of their own: one in each device's image of the
+// library, 0 when it is loaded.
+__device__ DeviceStatus g_kept_status;
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // Row pitch (elements) of the channel-major a, b, x sections. bf16 rows start on
@@ -160,6 +164,40 @@ int check_current_device(std::initializer_list<const void *> ptrs, const char *w
             return TRIMUL_ERR_INVALID_ARG;
         }
     }
+    return TRIMUL_OK;
+}
+
+// ---- status words --------------------------------------------------------------
+
+constexpr size_t kStatusBytes = sizeof(DeviceStatus);
+static_assert(sizeof(DeviceStatus) == 16, "the size that trimul.h states");
+
+DeviceStatus *status_of(void *status, void *workspace) { return static_cast<DeviceStatus *>(status ? status : workspace); }
+
+int read_status(const void *word, cudaStream_t s, int *detail) {
+    DeviceStatus st;
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess) e = cudaMemcpy(&st, word, sizeof st, cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) {
+        set_detail("status read", e);
+        return TRIMUL_ERR_CUDA;
+    }
+    if (detail) {
+        detail[0] = st.code;
+        detail[1] = st.site;
+        detail[2] = st.block;
+        detail[3] = st.aux;
+    }
+    if (st.code == DEV_OK) return TRIMUL_OK;
+    return st.code == DEV_TIMEOUT ? TRIMUL_ERR_TIMEOUT : TRIMUL_ERR_DEVICE;
+}
+
+// A caller's own status word: aligned, and no memory of the call's tensors.
+int check_status(const void *status, std::initializer_list<std::pair<const void *, size_t>> tensors) {
+    if (!status) return TRIMUL_OK;
+    if (!aligned(status, 16)) return TRIMUL_ERR_MISALIGNED;
+    for (const auto &t : tensors)
+        if (overlap(status, kStatusBytes, t.first, t.second)) return TRIMUL_ERR_ALIAS;
     return TRIMUL_OK;
 }
 
@@ -1115,7 +1153,7 @@ int check_attn(const atomattn_params *p, const void *out) {
     for (const void *v : al16)
         if (v && !aligned(v, 16)) return TRIMUL_ERR_MISALIGNED;
     if (p->atom_mask && !aligned(p->atom_mask, 2)) return TRIMUL_ERR_MISALIGNED;
-    if (!p->workspace || p->workspace_bytes < atomattn_workspace_size()) return TRIMUL_ERR_WORKSPACE;
+    if (!p->status && (!p->workspace || p->workspace_bytes < atomattn_workspace_size())) return TRIMUL_ERR_WORKSPACE;
     if (!aligned(p->workspace, 256)) return TRIMUL_ERR_MISALIGNED;
     const size_t n = attn_elems(p) * 2;
     const size_t nb = (size_t)p->batch * attn_windows(p) * p->heads * 32 * 128 * 2;
@@ -1124,7 +1162,7 @@ int check_attn(const atomattn_params *p, const void *out) {
         overlap(out, n, p->bias, nb) || overlap(out, n, p->atom_mask, nm) ||
         overlap(out, n, p->workspace, p->workspace_bytes))
         return TRIMUL_ERR_ALIAS;
-    return TRIMUL_OK;
+    return check_status(p->status, {{out, n}, {p->q, n}, {p->k, n}, {p->v, n}, {p->bias, nb}, {p->atom_mask, nm}});
 }
 
 int check_attn_backward(const atomattn_params *p, const void *dout, const atomattn_grads *g) {
@@ -1147,7 +1185,7 @@ int check_attn_backward(const atomattn_params *p, const void *dout, const atomat
         for (int j = i + 1; j < 5; ++j)
             if (overlap(out[i].first, out[i].second, out[j].first, out[j].second)) return TRIMUL_ERR_ALIAS;
     }
-    return TRIMUL_OK;
+    return check_status(p->status, {{dout, n}, {g->dk, n}, {g->dv, n}, {g->dbias, nb}});  // the rest: check_attn
 }
 
 // q, k or v [batch][n][heads][32] as (heads * 32, n, batch): boxes of one head's 32 elements
@@ -1274,7 +1312,8 @@ bool linear_sizes_ok(long long rows, int k, int n) {
 int check_linear(const trimul_linear_params *p, size_t need) {
     if (!p->weight) return TRIMUL_ERR_INVALID_ARG;
     if (!aligned(p->weight, 16) || (p->bias && !aligned(p->bias, 2))) return TRIMUL_ERR_MISALIGNED;
-    if (!p->workspace || p->workspace_bytes < need) return TRIMUL_ERR_WORKSPACE;
+    // (With a status word elsewhere, a workspace that would hold nothing else may be missing.)
+    if (!(p->status && need <= kHeader) && (!p->workspace || p->workspace_bytes < need)) return TRIMUL_ERR_WORKSPACE;
     if (!aligned(p->workspace, 256)) return TRIMUL_ERR_MISALIGNED;
     return TRIMUL_OK;
 }
@@ -1288,7 +1327,7 @@ int check_linear_sizes(const trimul_linear_params *p) {
 
 KernelCtl linear_ctl(const trimul_linear_params *p) {
     KernelCtl c;
-    c.status = static_cast<DeviceStatus *>(p->workspace);
+    c.status = status_of(p->status, p->workspace);
     c.timeout_ns = (unsigned long long)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
     c.debug_flags = 0;
     return c;
@@ -1391,7 +1430,7 @@ int run_linear_one_pass(const void *x, const trimul_act8 *x8, const void *dy, co
         a.partial = reinterpret_cast<float *>(base + L.partial);
         a.sums = reinterpret_cast<float *>(base + L.sums);
     }
-    a.clear_status = 1;
+    a.clear_status = p->status == nullptr;
     a.ctl = ctl;
     if (int rc = cuda_rc(launch_linear_bwd(m, a, x8 != nullptr, teams, s), "linear_bwd launch")) return rc;
     if (teams == 1) return TRIMUL_OK;
@@ -1659,22 +1698,49 @@ int trimul_device_status(const trimul_params *p, trimul_stream_t stream, int *de
         if (int rc = noalloc_scratch_address(&scratch)) return rc;
         word = scratch;
     }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    DeviceStatus st;
-    cudaError_t e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess) e = cudaMemcpy(&st, word, sizeof st, cudaMemcpyDeviceToHost);
+    return read_status(word, reinterpret_cast<cudaStream_t>(stream), detail);
+}
+
+int trimul_status_word(void **word) {
+    static void *at[kMaxDevices];
+    static std::mutex mu;
+    if (!word) return TRIMUL_ERR_INVALID_ARG;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) return TRIMUL_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lk(mu);
+    if (e == cudaSuccess && !at[dev]) {
+        // Looked up once per device. Loading the library's image for that may allocate, which a
+        // capture need not forbid: nothing of it is captured.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) == cudaSuccess) {
+            e = cudaGetSymbolAddress(&at[dev], g_kept_status);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+        }
+    }
     if (e != cudaSuccess) {
-        set_detail("status read", e);
+        cudaGetLastError();
+        set_detail("status word", e);
         return TRIMUL_ERR_CUDA;
     }
-    if (detail) {
-        detail[0] = st.code;
-        detail[1] = st.site;
-        detail[2] = st.block;
-        detail[3] = st.aux;
+    *word = at[dev];
+    return TRIMUL_OK;
+}
+
+int trimul_status_take(void *word, trimul_stream_t stream, int *detail) {
+    if (!word) return TRIMUL_ERR_INVALID_ARG;
+    if (!aligned(word, 16)) return TRIMUL_ERR_MISALIGNED;
+    if (int rc = check_device_ptr(word, "status word")) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int rc = read_status(word, s, detail);
+    if (rc != TRIMUL_ERR_TIMEOUT && rc != TRIMUL_ERR_DEVICE) return rc;
+    cudaError_t e = cudaMemsetAsync(word, 0, kStatusBytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) {
+        set_detail("status clear", e);
+        return TRIMUL_ERR_CUDA;
     }
-    if (st.code == DEV_OK) return TRIMUL_OK;
-    return st.code == DEV_TIMEOUT ? TRIMUL_ERR_TIMEOUT : TRIMUL_ERR_DEVICE;
+    return rc;
 }
 
 size_t trimul_backward_workspace_size(int N, int c_z, int c_h) {
@@ -1713,11 +1779,11 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
     if ((rc = check_attn(p, out))) return rc;
     const DevState *d = nullptr;
     if ((rc = device_state(&d, true))) return rc;
-    const void *ptrs[] = {p->q, p->k, p->v, p->bias, p->atom_mask, p->workspace, out};
+    const void *ptrs[] = {p->q, p->k, p->v, p->bias, p->atom_mask, p->workspace, p->status, out};
     for (const void *v : ptrs)
         if ((rc = check_device_ptr(v, "atom attention pointer"))) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // The kernel clears the status word itself (CTA 0, after its setup barrier).
+    // The kernel clears the workspace's status word itself (CTA 0, after its setup barrier).
     AttnMaps m;
     if ((rc = map_attn(&m.q, p->q, p, 128)) || (rc = map_attn(&m.k, p->k, p, 224)) ||
         (rc = map_attn(&m.v, p->v, p, 256)))
@@ -1735,7 +1801,8 @@ int atomattn_forward(const atomattn_params *p, void *out, trimul_stream_t stream
     a.mask = static_cast<const __nv_bfloat16 *>(p->atom_mask);
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.scale = 0.17677669529663687f;  // 1 / sqrt(32)
-    a.ctl.status = static_cast<DeviceStatus *>(p->workspace);
+    a.clear_status = p->status == nullptr;
+    a.ctl.status = status_of(p->status, p->workspace);
     a.ctl.timeout_ns = (unsigned long long)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
     a.ctl.debug_flags = 0;
     const int grid = a.units < d->sms ? (int)a.units : d->sms;
@@ -1747,8 +1814,8 @@ int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn
     if ((rc = check_attn_backward(p, dout, g))) return rc;
     const DevState *d = nullptr;
     if ((rc = device_state(&d, true))) return rc;
-    if ((rc = check_current_device({p->q, p->k, p->v, p->bias, p->atom_mask, p->workspace, dout, g->dq, g->dk, g->dv,
-                                    g->dbias},
+    if ((rc = check_current_device({p->q, p->k, p->v, p->bias, p->atom_mask, p->workspace, p->status, dout, g->dq, g->dk,
+                                    g->dv, g->dbias},
                                    "atom attention pointer")))
         return rc;
     AttnBwdMaps m;
@@ -1771,29 +1838,16 @@ int atomattn_backward(const atomattn_params *p, const void *dout, const atomattn
     a.dk = static_cast<__nv_bfloat16 *>(g->dk);
     a.dv = static_cast<__nv_bfloat16 *>(g->dv);
     a.scale = 0.17677669529663687f;  // 1 / sqrt(32)
-    a.ctl.status = static_cast<DeviceStatus *>(p->workspace);
+    a.clear_status = p->status == nullptr;
+    a.ctl.status = status_of(p->status, p->workspace);
     a.ctl.timeout_ns = (unsigned long long)(p->timeout_ms ? p->timeout_ms : 2000u) * 1000000ull;
     a.ctl.debug_flags = 0;
     return cuda_rc(launch_atomattn_bwd(m, a, d->sms, reinterpret_cast<cudaStream_t>(stream)), "atomattn_bwd launch");
 }
 
 int atomattn_device_status(const atomattn_params *p, trimul_stream_t stream, int *detail) {
-    if (!p || !p->workspace) return TRIMUL_ERR_INVALID_ARG;
-    DeviceStatus st;
-    cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = cudaMemcpy(&st, p->workspace, sizeof st, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) {
-        set_detail("status read", e);
-        return TRIMUL_ERR_CUDA;
-    }
-    if (detail) {
-        detail[0] = st.code;
-        detail[1] = st.site;
-        detail[2] = st.block;
-        detail[3] = st.aux;
-    }
-    if (st.code == DEV_OK) return TRIMUL_OK;
-    return st.code == DEV_TIMEOUT ? TRIMUL_ERR_TIMEOUT : TRIMUL_ERR_DEVICE;
+    if (!p || !status_of(p->status, p->workspace)) return TRIMUL_ERR_INVALID_ARG;
+    return read_status(status_of(p->status, p->workspace), reinterpret_cast<cudaStream_t>(stream), detail);
 }
 
 // ---- linear layers and activations in 8 bits (include/linear.h) ----------------------
@@ -1816,11 +1870,13 @@ int trimul_linear_forward(const void *x, const void *residual, const trimul_line
         overlap(p->workspace, kHeader, x, xn) || overlap(p->workspace, kHeader, residual, yn) ||
         overlap(p->workspace, kHeader, p->weight, wn) || overlap(p->workspace, kHeader, p->bias, bn))
         return TRIMUL_ERR_ALIAS;
+    if ((rc = check_status(p->status, {{x, xn}, {residual, yn}, {y, yn}, {p->weight, wn}, {p->bias, bn}}))) return rc;
     const DevState *d = nullptr;
     if ((rc = device_state(&d, true))) return rc;
-    if ((rc = check_current_device({x, residual, y, p->weight, p->bias, p->workspace}, "linear pointer"))) return rc;
+    if ((rc = check_current_device({x, residual, y, p->weight, p->bias, p->workspace, p->status}, "linear pointer"))) return rc;
     return run_linear(LIN_FWD, x, p->weight, 0, residual, y, (int)p->rows, p->out_features, p->in_features, p->act,
-                      p->bias, nullptr, nullptr, true, false, false, linear_ctl(p), reinterpret_cast<cudaStream_t>(stream));
+                      p->bias, nullptr, nullptr, p->status == nullptr, false, false, linear_ctl(p),
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t trimul_linear_backward_workspace_size(long long rows, int in_features, int out_features, int act, int from8) {
@@ -1854,16 +1910,17 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
         for (int j = i + 1; j < 4; ++j)
             if (overlap(out[i].first, out[i].second, out[j].first, out[j].second)) return TRIMUL_ERR_ALIAS;
     }
+    if ((rc = check_status(p->status, {in[0], in[1], in[2], in[3], in[4], in[5], out[0], out[1], out[2], out[3]}))) return rc;
     const DevState *d = nullptr;
     if ((rc = device_state(&d, true))) return rc;
-    if ((rc = check_current_device({x, codes, scales, dy, dx, dw, db, p->weight, p->bias, p->workspace},
+    if ((rc = check_current_device({x, codes, scales, dy, dx, dw, db, p->weight, p->bias, p->workspace, p->status},
                                    "linear pointer")))
         return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *base = static_cast<uint8_t *>(p->workspace);
     const KernelCtl ctl = linear_ctl(p);
     if ((dx || dw || db) && linear_one_pass(k, n)) return run_linear_one_pass(x, x8, dy, p, dx, dw, db, L, ctl, s);
-    bool clear = true;   // the call's first tensor kernel clears the status word
+    bool clear = p->status == nullptr;  // the call's first tensor kernel clears the workspace's status word
     bool after = false;  // a kernel of this call has been launched
     const bool d_pass = act != TRIMUL_ACT_NONE && (dx || dw || db);
     if (x8 && (dw || db || d_pass)) {
@@ -1928,6 +1985,7 @@ int trimul_linear_device_status(const trimul_linear_params *p, trimul_stream_t s
     atomattn_params q;
     memset(&q, 0, sizeof q);
     q.workspace = p->workspace;
+    q.status = p->status;
     return atomattn_device_status(&q, stream, detail);
 }
 

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
+    if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 
     // Loads of window s: its q, dO and bias into stage (s - first) % kStages, and the key group
     // s + 3 (for the block's first window all four groups) into ring slot (group - first) % RING.

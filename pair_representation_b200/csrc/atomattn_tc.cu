@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(aa::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     // The call starts here: CTA 0 clears the status word (every failure is recorded by a
     // bounded wait after ctl.timeout_ns, long after all CTAs of this one-wave grid started).
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
+    if (args.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *ctl.status = DeviceStatus{0, 0, 0, 0};
 
     if (warp == WORKER_WARPS) {
         if (lane == 0) {

@@ -254,6 +254,7 @@ struct AttnArgs {
     const __nv_bfloat16 *mask;  // [batch][n] or null
     __nv_bfloat16 *out;         // [batch][n][heads][32]
     float scale;                // 1 / sqrt(32)
+    int clear_status;
     KernelCtl ctl;
 };
 
@@ -275,6 +276,7 @@ struct AttnBwdArgs {
     __nv_bfloat16 *dk, *dv;           // [batch][n][heads][32]
     float scale;                      // 1 / sqrt(32)
     int per_chain, chains;            // set by the launcher: key groups per block, blocks per (batch, head)
+    int clear_status;
     KernelCtl ctl;
 };
 

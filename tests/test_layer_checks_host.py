@@ -55,3 +55,37 @@ def test_the_layer_refuses_a_bias_or_mask_of_another_shape(case, monkeypatch):
     for call in (lambda: layer(x, bias, mask), lambda: layer.backward(x, x, bias, mask)):
         with pytest.raises(ValueError, match="must be"):
             call()
+
+
+BASE = 1 << 32  # fake device addresses: never dereferenced by host checks
+X, Y, W, B, WS, DY, DX, DW, DB, ST = (BASE + (i << 28) for i in range(1, 11))
+
+
+def test_a_status_word_of_the_callers():
+    """Aligned and apart from the tensors; a call that needs no scratch then needs no workspace."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    E = tm.ERR
+    passed = [E["TRIMUL_ERR_CUDA"], E["TRIMUL_ERR_UNSUPPORTED"]]  # what a valid call returns where there is no GPU
+
+    def calls(rows, status, ws=None, size=0):
+        p = tm.LinearParams(rows, 128, 64, 3, W, B, ws, size, 0, status)
+        a = tm.AtomAttnParams(2, 100, 4, 32, X, Y, W, B, None, ws, size, 0, status)
+        yield tm.trimul_linear_forward(X, None, p, DX, stream=0, check=False)
+        yield tm.trimul_linear_backward(X, None, DY, p, DX, DW, DB, stream=0, check=False)
+        yield tm.atomattn_forward(a, DX, stream=0, check=False)
+        yield tm.atomattn_backward(a, DY, tm.AtomAttnGrads(DX, DW, DB, None), stream=0, check=False)
+
+    assert all(rc in passed for rc in calls(100, ST))
+    assert list(calls(100, None)) == [E["TRIMUL_ERR_WORKSPACE"]] * 4
+    assert list(calls(100, ST + 8)) == [E["TRIMUL_ERR_MISALIGNED"]] * 4
+    assert list(calls(100, DX + 16)) == [E["TRIMUL_ERR_ALIAS"]] * 4
+    assert list(calls(100, X + 16)) == [E["TRIMUL_ERR_ALIAS"]] * 4
+    rcs = list(calls(100000, ST))
+    assert rcs[1] == E["TRIMUL_ERR_WORKSPACE"] and all(rc in passed for rc in rcs[:1] + rcs[2:])
+    need = tm.trimul_linear_backward_workspace_size(100000, 128, 64, 3)
+    assert all(rc in passed for rc in calls(100000, ST, WS, need))
+    assert list(calls(100000, WS + 512, WS, need))[1] == E["TRIMUL_ERR_ALIAS"]
+    assert tm.lib().trimul_status_word(None) == E["TRIMUL_ERR_INVALID_ARG"]
+    assert tm.lib().trimul_status_take(None, None, None) == E["TRIMUL_ERR_INVALID_ARG"]
+    assert tm.lib().trimul_status_take(ST + 4, None, None) == E["TRIMUL_ERR_MISALIGNED"]
