@@ -25,8 +25,9 @@
  * D is dy or 0, exactly); db sums D before that rounding. Where p is so near 0
  * that its sums' rounding could turn its sign (under a bound from the norms of its
  * rows of x and W), relu' takes p again in 64 bits: the sign is right down to
- * 2^-53 of the products' sizes. Gradients have the parameters' type. Every sum is taken in a fixed order, so equal calls give equal
- * bits.
+ * 2^-53 of the products' sizes. Gradients have the parameters' type. Sums over the
+ * rows are taken in parts of at most 65536 rows each, and the parts added in fp32.
+ * Every sum is taken in a fixed order, so equal calls give equal bits.
  *
  * Ownership, threading and errors follow trimul.h: the caller owns every buffer,
  * a call enqueues on `stream` and returns TRIMUL_OK or a negative trimul_status,

@@ -1229,6 +1229,11 @@ int linear_bn(long long M, int N) {
 // 512 rows (8 K blocks), where adding the parts up in a second launch costs what their length saves or more
 // (backward with silu, one part and several: 512 x 1024 -> 1024 31 and 33 us, 512 x 512 -> 352 25 and 25;
 // 1024 x 512 -> 352 29 and 25).
+//
+// No part is longer than kSumRows rows, in the one-pass form and for D's column sums as well: the tensor core cuts each
+// step of a sum (16 rows) at 2^-23 towards 0, so terms of one sign lose up to 2^-24 of their sum a step on average:
+// 4096 steps 2^-12, a sixteenth of the largest rounding to bf16. The parts are added in fp32, rounded to nearest.
+constexpr int kSumRows = 65536;
 struct LinearSplit {
     int tiles, splits, per;  // 128 x 128 tiles of dW, parts, K blocks of 64 rows per part
 };
@@ -1239,6 +1244,8 @@ LinearSplit linear_split(long long rows, int k, int n) {
     int want = kLinearCtas / s.tiles;
     if (want < 1 || kb <= 8) want = 1;
     if (want > kb) want = kb;
+    const int least = ceil_div(kb, kSumRows / 64);
+    if (want < least) want = least;
     s.per = ceil_div(kb, want);
     s.splits = ceil_div(kb, s.per);
     return s;
@@ -1250,7 +1257,8 @@ LinearSplit linear_split(long long rows, int k, int n) {
 bool linear_one_pass(int k, int n) { return k <= 128 && n <= 512; }
 int linear_teams(long long rows, int n) {
     const int tiles = ceil_div(rows, 128), most = n > 256 ? kLinearCtas / 2 : kLinearCtas;
-    return tiles < most ? tiles : most;
+    const int waves = ceil_div(tiles, (long long)most * (kSumRows / 128));  // whole waves of teams, one after the other
+    return tiles < most ? tiles : most * waves;
 }
 
 // Height of LIN_FWD's row tiles in units of 128: two where B is streamed beside A, so that B's blocks serve
@@ -1267,8 +1275,13 @@ int linear_high(long long M, int N, int K) {
 
 // The groups of CTAs that take row tiles in turn in a product of M x N (LIN_FWD, LIN_GRAD).
 int linear_groups(long long M, int N, int high) {
-    const int tiles = ceil_div(M, 128 * high), groups = kLinearCtas / ceil_div(N, linear_bn(M, N));
-    return groups < tiles ? groups : tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
+    const int tiles = ceil_div(M, 128 * high), most = kLinearCtas / ceil_div(N, linear_bn(M, N));
+    return most < tiles ? most : tiles;  // at least 1: at most 128 column tiles (kMaxFeatures)
+}
+// LIN_GRAD's, which sum columns over their tiles.
+int linear_sum_groups(long long M, int N) {
+    const int groups = linear_groups(M, N, 1), waves = ceil_div(ceil_div(M, 128), (long long)groups * (kSumRows / 128));
+    return groups * waves;
 }
 
 // Sections of the backward workspace (byte offsets, 256-byte aligned).
@@ -1296,7 +1309,7 @@ LinearBwdLayout linear_bwd_layout(long long rows, int k, int n, int act, int fro
         const LinearSplit s = linear_split(rows, k, n);
         if (s.splits > 1) L.partial = take((size_t)s.splits * n * k * 4);  // dW of each part, fp32
         // Column sums of D: four per row-tile group of the D product, or one row per part of dW.
-        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * linear_groups(rows, n, 1) : s.splits > 1 ? (size_t)s.splits : 0;
+        const size_t sums = act != TRIMUL_ACT_NONE ? (size_t)4 * linear_sum_groups(rows, n) : s.splits > 1 ? (size_t)s.splits : 0;
         L.sums = take(sums * n * 4);
         // dW where only db is wanted and its sums come with the product.
         L.scrap = take(s.splits == 1 && act == TRIMUL_ACT_NONE ? (size_t)n * k * 2 : 0);
@@ -1347,7 +1360,7 @@ int map_blocks(CUtensorMap *m, const void *t, int cols, int rows) {
 }
 
 // Y [M][N] = epilogue(A [M][K] B^T), B [N][K] or (b_mn) [K][N]. LIN_GRAD: sums has four rows for each
-// of linear_groups(M, N, 1), or where there is one group db itself is written too.
+// of linear_sum_groups(M, N), or where there is one group db itself is written too.
 int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, void *Y, int M, int N, int K, int act,
                const void *bias, float *sums, void *db, bool clear, bool after, bool more, const KernelCtl &ctl,
                cudaStream_t s) {
@@ -1368,7 +1381,7 @@ int run_linear(int mode, const void *A, const void *B, int b_mn, const void *E, 
     a.row_tiles = ceil_div(M, 128 * a.high);
     a.col_tiles = ceil_div(N, bn);
     a.kblocks = ceil_div(K, 64);
-    a.groups = linear_groups(M, N, a.high);
+    a.groups = mode == LIN_GRAD ? linear_sum_groups(M, N) : linear_groups(M, N, a.high);
     a.splits = 1;
     a.kb_per_split = a.kblocks;
     a.act = act;
@@ -1941,7 +1954,7 @@ int trimul_linear_backward(const void *x, const trimul_act8 *x8, const void *dy,
         D = base + L.d;
         clear = false;
         after = true;
-        const int groups = linear_groups(rows, n, 1);
+        const int groups = linear_sum_groups(rows, n);
         sum_rows = 4 * groups;
         db_done = groups == 1;
     }

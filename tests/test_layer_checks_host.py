@@ -89,3 +89,12 @@ def test_a_status_word_of_the_callers():
     assert tm.lib().trimul_status_word(None) == E["TRIMUL_ERR_INVALID_ARG"]
     assert tm.lib().trimul_status_take(None, None, None) == E["TRIMUL_ERR_INVALID_ARG"]
     assert tm.lib().trimul_status_take(ST + 4, None, None) == E["TRIMUL_ERR_MISALIGNED"]
+
+
+@pytest.mark.parametrize("k,n,act", [(8, 8, 0), (8, 8, 3), (128, 512, 1), (1280, 1280, 0), (160, 1280, 3), (4096, 4096, 0)])
+@pytest.mark.parametrize("rows", [65537, 1 << 20, 10000000, 1 << 30])
+def test_no_sum_over_more_rows_than_a_part(k, n, act, rows):
+    """dW of each part of at most 65536 rows has its place in the workspace, beside what the call needs anyhow."""
+    parts = -(-rows // 65536)
+    d = rows * n * 2 if act and (k > 128 or n > 512) else 0  # D, where it is a product of its own
+    assert tm.trimul_linear_backward_workspace_size(rows, k, n, act) >= 256 + d + parts * n * (k + 1) * 4
