@@ -468,6 +468,8 @@ def _run_on(index: int, stream, tensors, call):
     what the call allocates belongs to it. `tensors` may be another stream's: they are marked as
     used on this one, so that their memory is not handed out again before this work is done."""
     torch = _T or _load()
+    if stream is not None and not isinstance(stream, int) and stream.device.index != index:
+        raise ValueError(f"stream must be one of device {index}, where the tensors are")
     with torch.cuda.device(index):
         if stream is None:
             return call()
@@ -521,7 +523,8 @@ def atom_attention(q, k, v, bias=None, atom_mask=None, out=None, workspace=None,
     _need_bf16("atom_attention", index, (q, k, v, bias, atom_mask, out))
     if workspace is not None:
         _need_workspace("atom_attention", index, workspace)
-    if _current_device() != index or stream is not None and _stream(stream) != _raw_stream(index):
+    if _current_device() != index or stream is not None and (
+            _stream(stream) != _raw_stream(index) or not isinstance(stream, int) and stream.device.index != index):
         return _run_on(index, stream, (q, k, v, bias, atom_mask, out, workspace),
                        lambda: atom_attention(q, k, v, bias, atom_mask, out, workspace))
     if out is None:

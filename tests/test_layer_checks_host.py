@@ -98,3 +98,20 @@ def test_no_sum_over_more_rows_than_a_part(k, n, act, rows):
     parts = -(-rows // 65536)
     d = rows * n * 2 if act and (k > 128 or n > 512) else 0  # D, where it is a product of its own
     assert tm.trimul_linear_backward_workspace_size(rows, k, n, act) >= 256 + d + parts * n * (k + 1) * 4
+
+
+class _Stream:
+    """What the calls look at of a torch stream."""
+
+    def __init__(self, index):
+        self.device, self.cuda_stream = torch.device("cuda", index), 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Work on device 0's tensors has nothing to do on device 1's streams: the call had run on another stream than
+    the one it was given."""
+    monkeypatch.setattr(torch.cuda, "device", lambda index: pytest.fail("a device was entered"))
+    ran = []
+    with pytest.raises(ValueError, match="stream"):
+        tm._run_on(0, _Stream(1), (), lambda: ran.append(1))
+    assert not ran
