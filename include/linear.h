@@ -84,6 +84,7 @@ int trimul_linear_forward(const void *x, const void *residual, const trimul_line
  * own size while it lies within 2^-14 of its block's largest, except that a value
  * above 1.75 times its block's power of two becomes 1.75 times it (at most 1/8
  * lower). An infinity or NaN is kept as NaN and does not change its block's scale.
+ * (A scale byte of 255, which packing never writes, stands for NaN.)
  *
  * codes [rows][channels], scales [rows][channels / 32], one byte each, both 16-byte
  * aligned; channels a multiple of 32, at most 16384; 1 <= rows <= 2^30. */

@@ -12,15 +12,12 @@
 #include <cuda_fp8.h>
 
 #include "kernels.h"
+#include "linear_act.cuh"
 
 namespace trimul {
 namespace {
 
 constexpr int kThreads = 256, kUnroll = 4;
-
-__device__ __forceinline__ float scale_value(uint32_t s) {  // 2^(s - 127); s = 0: 2^-127, subnormal
-    return __uint_as_float(s ? s << 23 : 0x00400000u);
-}
 
 // The largest of two packed pairs of unsigned 16-bit values.
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -113,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(const uint2 *__re
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const long long i = base + (long long)u * kThreads;
-            const float size = scale_value(s[u]);
+            const float size = e8m0_value(s[u]);
             if (i < pieces)
                 x[i] = make_uint4(value2(c[u].x & 0xFFFFu, size), value2(c[u].x >> 16, size),
                                   value2(c[u].y & 0xFFFFu, size), value2(c[u].y >> 16, size));

@@ -1,4 +1,5 @@
-// linear_act.cuh - the activations of the linear layers and their slopes.
+// linear_act.cuh - the activations of the linear layers and their slopes, the bound that decides relu's sign, and
+// the value of an 8-bit activation's scale.
 //
 // exp(-p) and 1 / (1 + exp(-p)) come from the hardware's ex2 and rcp (relative errors about
 // 2^-22), far under the half step 2^-8 of the bf16 result. Those run at 16 a clock and SM, and at
@@ -111,6 +112,11 @@ __device__ __forceinline__ void act_grad4(float2 (&p)[2], const float2 (&d)[2]) 
             p[t] = __fmul2_rn(d[t], ACT == LIN_SIGMOID ? __fmul2_rn(s[t], c) : __ffma2_rn(__fmul2_rn(p[t], s[t]), c, s[t]));
         }
     }
+}
+
+// A scale byte's value: 2^(s - 127), at s = 0 a subnormal number; 255, which packing never writes, is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+    return __uint_as_float(s == 0u ? 0x00400000u : s == 255u ? 0x7FC00000u : s << 23);
 }
 
 // ---- the sign of relu's p -------------------------------------------------------------------------

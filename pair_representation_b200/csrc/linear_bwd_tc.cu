@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(lb::THREADS, 1)
             if (t > 0 && !warp_wait(xdone, (uint32_t)(t - 1) & 1u, abort_flag, ctl, SITE_LBW | 9, t)) return false;
             const uint32_t s = scale_next;
             scale_next = scale_of(t + 1);
-            const float size = __uint_as_float(s ? s << 23 : 0x00400000u);  // 2^(s - 127)
+            const float size = e8m0_value(s);
             const uint8_t *src = codes + (t % XB) * CODES + crow * 128;
             uint8_t *dst = xbuf + (cblk >> 1) * HALF + crow * 128;
             float squares = 0.f;
