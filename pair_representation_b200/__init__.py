@@ -880,6 +880,13 @@ class _TriangleMultiplication:
         p.debug_flags = self.debug_flags
         return p
 
+    def _mask(self, z, mask):
+        if mask is None:
+            return None
+        if mask.numel() != z.shape[0] * z.shape[1]:
+            raise ValueError("mask must be [N, N]")
+        return mask.to(dtype=self.dtype).contiguous()
+
     def __call__(self, z, mask=None, out=None, stream=None):
         import torch
         if z.dim() != 3 or z.shape[0] != z.shape[1] or z.shape[2] != self.c_z:
@@ -887,10 +894,11 @@ class _TriangleMultiplication:
         if z.dtype != self.dtype or z.device != self.device:
             raise ValueError("z must match the layer's dtype and device")
         z = z.contiguous()
-        if mask is not None:
-            mask = mask.to(dtype=self.dtype).contiguous()
+        mask = self._mask(z, mask)
         if out is None:
             out = torch.empty_like(z)
+        elif out.shape != z.shape or out.dtype != z.dtype or out.device != z.device or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of z's shape, dtype and device")
         p = self.params(z.shape[0])
         trimul_forward(z, mask, p, self.direction, out, stream)
         return out
@@ -918,8 +926,7 @@ class _TriangleMultiplication:
         if z.dtype != self.dtype or z.device != self.device or dout.shape != z.shape or dout.dtype != z.dtype:
             raise ValueError("z and dout must match each other and the layer's dtype and device")
         z, dout = z.contiguous(), dout.contiguous()
-        if mask is not None:
-            mask = mask.to(dtype=self.dtype).contiguous()
+        mask = self._mask(z, mask)
         N = z.shape[0]
         p = self.params(N)
         g = TrimulGrads()

@@ -115,3 +115,17 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="stream"):
         tm._run_on(0, _Stream(1), (), lambda: ran.append(1))
     assert not ran
+
+
+def test_the_triangle_layer_refuses_a_mask_or_out_of_another_size():
+    """The kernels take both sizes from z."""
+    layer = tm.TriangleMultiplicationOutgoing(128, 128)
+    layer.tensors, layer.dtype, layer.device = {}, BF16, torch.device("cpu")
+    z = torch.zeros(6, 6, 128, dtype=BF16)
+    for mask in (torch.ones(5, 6), torch.ones(6), torch.ones(0, 6)):
+        for call in (lambda: layer(z, mask), lambda: layer.backward(z, z, mask)):
+            with pytest.raises(ValueError, match="mask"):
+                call()
+    for out in (z[:5], z.float(), z.transpose(0, 1)):
+        with pytest.raises(ValueError, match="out"):
+            layer(z, None, out=out)
