@@ -6,9 +6,9 @@
 // two for each value they and the arithmetic around them, not memory, bound a wide layer's epilogue
 // (589824 x 128 -> 512 with silu: 226 us, without activation 137). So four values share one
 // reciprocal: of a b c d, times c d and then b it is 1 / a, and so on; 1.25 for each, and fewer
-// instructions too: 162 us. The product stays finite while all four p are over -21; where one of the
-// values a thread has in hand is not, or is NaN, each takes its own (at p of size 11, where most threads
-// have such a value, the same call takes 273 us).
+// instructions too: 162 us (short runs at full clock, here and below). The product stays finite while
+// all four p are over -21; where one of the values a thread has in hand is not, or is NaN, each takes
+// its own (at p of size 11, where most threads have such a value, the same call takes 273 us).
 #pragma once
 
 #include "kernels.h"
@@ -129,8 +129,8 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
 // x or W has bound 0, and is never asked for. At normal inputs about 5 in 10^5 places for 128
 // products, 1 in 10^3 for 1024, 7 in 100 for 16384. The backward with relu, against a bound from the sums
 // themselves, which missed signs where they cancel: 147456 x 128 -> 128 39 -> 44 us, x in 8 bits 45 -> 50, -> 512
-// 125 -> 128; 147456 x 512 -> 128 138 -> 153; 28000 x 1024 -> 1024 243 -> 294; 3605 x 328 -> 200 26.6 -> 28.7; 3000 x
-// 16384 -> 256 296 -> 1980 (all cold; with a fifth of the rows 0 44 us where it had been 758).
+// 125 -> 128; 147456 x 512 -> 128 138 -> 155; 28000 x 1024 -> 1024 243 -> 281; 3605 x 328 -> 200 26.6 -> 28.7; 3000 x
+// 16384 -> 256 296 -> 1130 (inputs cold in L2; with a fifth of the rows 0 the first is 44 us as well, and was 758).
 __device__ __forceinline__ float sign_bound(int k) { return (float)((k + 15) / 16) * (6.f * 1.1920929e-7f) * 1.0625f; }
 
 // A row's norm from its sum of squares. Squares under 2^-126 may be lost, and products in p too: any norm but 0

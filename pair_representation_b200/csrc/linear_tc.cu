@@ -11,6 +11,9 @@
 // forward reads x and W K-major, dx = D W reads W MN-major, dW = D^T x reads both
 // MN-major with the rows of the batch as the contracted index.
 //
+// LIN_GRAD rounds Y to bf16, the products' operand type: dx and dW are then off by 0.0024 of their norm, against 0.0017
+// of their own rounding alone (2^-8 at most for each).
+//
 // What bounds it: at the widths of a pair or atom representation (128 to 512 channels)
 // a row moves 2 (k + n) bytes for 2 k n operations, under the card's ratio of about 260
 // operations per byte, so the batch's rows are streamed once and everything else stays
@@ -23,9 +26,10 @@
 // overlaps the loads and MMAs of the next. E blocks arrive by TMA in the very buffer
 // the result leaves from, one block ahead.
 //
-// Measured: 147456 x 512 -> 128 with a residual 40 us (5.7 TB/s); 589824 x 128 -> 512 137 us
-// (5.5 TB/s), with silu 163 us at 1965 MHz (190 at the 1650 MHz that the power cap leaves in long runs):
-// the drain warps then issue at 54 % of their slots and wait on exponentials and shared memory.
+// Measured, call after call on the same inputs (and one call on inputs cold in L2): 147456 x 512 -> 128 with a
+// residual 38 us, 6.0 TB/s (48); 589824 x 128 -> 512 133 us, 5.7 TB/s (137), with silu 160 (170) at 1965 MHz and
+// 190 at the 1650 MHz that the power cap leaves in long runs: the drain warps then issue at 54 % of their slots and
+// wait on exponentials and shared memory.
 // Sixteen warps on blocks of 32 columns (eight on 64 columns: 188 us).
 //
 // Every wait is bounded; on a timeout the CTA lets its copies land and returns.
@@ -177,6 +181,7 @@ __device__ __forceinline__ void finish_row_relu_grad(float2 (&v)[16], const floa
             const int j = __ffs(left) - 1;
             const __nv_bfloat16 *wr = a.w + (size_t)(col0 + j) * a.K;
             double sum = 0.0;
+#pragma unroll 4
             for (int k = 8 * lane; k < a.K; k += 256) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(xr + k), w = *reinterpret_cast<const uint4 *>(wr + k);
                 sum += (pair_product(x.x, w.x) + pair_product(x.y, w.y)) + (pair_product(x.z, w.z) + pair_product(x.w, w.w));
