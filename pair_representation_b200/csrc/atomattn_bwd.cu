@@ -28,7 +28,8 @@
 // dS there too. Keeping dk and dv in registers instead took 64 of them per lane: two blocks
 // an SM fitted then, four do now (8 x 18432 atoms, 4 heads: 309 -> 168 us).
 //
-// Measured, the same size: 149 us with bias (3.8 TB/s), of which DRAM is busy 45 %; the shared-memory
+// Measured, the same size, call after call on the same inputs (and one call on inputs cold in L2): 144 us with bias,
+// 3.9 TB/s (154), 152 (161) with 5 % of the atoms masked as well. DRAM is busy 45 %; the shared-memory
 // pipe 61 %, the issue slots 45 %. A window's phases depend on each other, and four warps a scheduler
 // do not cover that.
 //
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(ab::THREADS, ab::kBlocks)
             }
         }
         __syncwarp();
-        // P and dS, each rounded once to bf16, the type of the products' other operands.
+        // P and dS, each rounded once to bf16, the type of the products' other operands (the gradients are then off by
+        // 0.0024 of their norm, against 0.0017 of their own rounding alone).
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             uint32_t pb[4][2], ds[4][2];
