@@ -15,7 +15,8 @@
  *   a slot is valid when its atom lies in [0, n_atoms) and its atom_mask is not
  *   0; a query with no valid slot gets 0.
  *
- * The projections around this core are per-atom Linear layers (linear.h).
+ * The projections around this core are per-atom Linear layers (linear.h); gating is
+ * not part of the library.
  *
  * Layouts (row-major, contiguous, bf16):
  *   q, k, v, out  [batch][n_atoms][heads][32]

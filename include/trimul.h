@@ -30,7 +30,9 @@
  * synchronise in trimul_forward or the stage calls: work is enqueued on
  * `stream` and the call returns. Its only global state is per-device launch
  * configuration (maximum shared memory attribute, SM count, cached driver
- * entry point), set up once and guarded for concurrent callers.
+ * entry point), set up once and guarded for concurrent callers, and in each
+ * device's image the scratch of trimul_forward_noalloc and a status word
+ * (trimul_status_word).
  *
  * Errors: every call returns TRIMUL_OK (0) or a negative code; no exception
  * crosses this boundary. Argument errors are detected on the host before any
